@@ -7,14 +7,16 @@ import os
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libkda_b200.so")
 
-KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_TIMEOUT = range(5)
+KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_TIMEOUT, KDA_ERR_BAD_PAGE = range(6)
 KDA_F32, KDA_BF16 = 0, 1
 
 # every symbol include/kda.h declares
 EXPORTED = ("kda_chunk_fwd", "kda_chunk_fwd_workspace_size", "kda_chunk_fwd_static_ws", "kda_recurrent_fwd",
             "kda_decode_step", "gdn_chunk_fwd", "gdn_recurrent_fwd", "gdn_decode_step", "kda_chunk_fwd_fused",
             "kda_decode_step_fused", "kda_status_string", "kda_get_last_device_error", "kda_version",
-            "kda_testing_set_chunk_fault", "kda_chunk_bwd", "kda_chunk_bwd_workspace_size")
+            "kda_testing_set_chunk_fault", "kda_chunk_bwd", "kda_chunk_bwd_workspace_size", "kda_attn_fwd",
+            "kda_attn_bwd", "kda_attn_bwd_workspace_size", "kda_kv_append", "kda_attn_decode_step",
+            "kda_attn_decode_workspace_size")
 
 _lib = None
 
@@ -67,6 +69,18 @@ def load() -> ctypes.CDLL:
     lib.kda_chunk_bwd_workspace_size.argtypes = [i32, i32, ctypes.c_int64, i32, i32, i32,
                                                  ctypes.POINTER(ctypes.c_size_t)]
     lib.kda_chunk_bwd_workspace_size.restype = ctypes.c_int
+    i64, f32, size_p = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(ctypes.c_size_t)
+    prompt_args = [vp, vp, vp, i64, i64, i64, vp, vp] + [i32] * 8 + [f32, ctypes.c_int]
+    lib.kda_attn_fwd.argtypes = prompt_args + [vp, vp, vp]
+    lib.kda_attn_bwd.argtypes = prompt_args + [vp] * 7 + [ctypes.c_size_t, vp]
+    lib.kda_attn_bwd_workspace_size.argtypes = [i32, i32, i32, size_p]
+    lib.kda_kv_append.argtypes = [vp, vp, vp, i64, i64, i64, vp, i32, i32, vp] + [i32] * 6 + \
+        [ctypes.c_int, vp, vp, i64, i32, vp, vp, i64, i64, i32, i32, vp, vp, vp]
+    lib.kda_attn_decode_step.argtypes = [vp, i64, vp, vp, i64, i64, i32, i32, vp, i64, i32, vp, i32, i32, i32, i32, f32,
+                                         ctypes.c_int, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.kda_attn_decode_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.c_int, size_p]
+    for name in EXPORTED[-6:]:
+        getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
 

@@ -1,0 +1,475 @@
+// attn_decode.cuh -- attention of one new token per sequence over a paged key-value cache.
+//
+//     o_h = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q_h . k_j - m),   j = 0 .. seq_lens[b] - 1,
+// one pass over the keys and values with a running maximum m and sum; the query heads of a group share
+// a head of the cache, so a block handles up to GC of them against keys it has loaded once.
+//
+// Bound by memory: the cache is read once.  The work of all (sequence, head) pairs is one line of tiles
+// of 64 tokens, cut into equal shares, one per block: long and short sequences balance, and a single
+// long sequence spreads over the whole GPU.  A share may begin and end inside a pair; such a pair's
+// blocks leave (m, sum, o) in the workspace and a second small kernel joins them in a fixed order (no
+// atomics: the same call gives the same bits).  The lengths stay on the device: every block works out its share from them.
+//
+// Inside a block each warp runs on its own: it takes 16 of a tile's 64 tokens and copies them through
+// its own ring of stages (cp.async, rows looked up page by page, rows past the end or on a bad page
+// filled with zeros), so there is no barrier but at the end of a pair, where the warps' results join.
+#pragma once
+
+#include "attn_common.cuh"
+
+namespace kda {
+namespace attn {
+
+constexpr int kDecodeWarps = 4;
+constexpr int kWarpTokens = 16;
+constexpr int kDecodeTile = kDecodeWarps * kWarpTokens;
+
+struct DecodeArgs {
+    const void *q;
+    int64_t q_stride;   // elements from one sequence's query to the next's
+    Cache cache;
+    const int32_t *lens;
+    int n, Hq, Hkv;
+    int vheads;         // head groups of at most GC query heads: Hkv * ceil(Hq / Hkv / GC)
+    float scale;
+    void *out;
+    float *lse;         // [n][Hq] or null
+    float *part;        // workspace: 2 slots per block of [GC][D + 2]
+    int blocks;         // blocks of the main kernel
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Tokens of sequence b that there are: its length, at most what its row of the table can hold.
+__device__ __forceinline__ int decode_len(const DecodeArgs &a, int b) {
+    const int64_t most = (int64_t)a.cache.width << a.cache.page_log2;
+    return (int)min((int64_t)max(__ldg(a.lens + b), 0), most);
+}
+__device__ __forceinline__ int decode_tiles(const DecodeArgs &a, int b) {
+    return (decode_len(a, b) + kDecodeTile - 1) / kDecodeTile;
+}
+
+// Where the line of tiles stands before sequence b_stop, and (out) its whole length, in tiles of one
+// head group.  Every thread of the block calls it and gets the same answer.
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    __syncthreads();
+    if (lane == 0) scratch[warp] = x;
+    __syncthreads();
+    x = 0;
+    for (int w = 0; w < warps; ++w) x += scratch[w];
+    return x;
+}
+
+// First sequence whose tiles reach beyond `want` (in tiles of one head group), and the tiles before it.
+__device__ __forceinline__ void find_sequence(const DecodeArgs &a, int64_t want, int64_t *scratch, int &seq,
+                                              int64_t &before) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int64_t at = 0;
+    for (int base = 0; base < a.n; base += blockDim.x) {
+        const int b = base + threadIdx.x;
+        const int64_t mine = b < a.n ? decode_tiles(a, b) : 0;
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        __syncthreads();
+        if (lane == 31) scratch[warp] = upto;
+        __syncthreads();
+        int64_t off = at, all = 0;
+        for (int w = 0; w < warps; ++w) {
+            if (w < warp) off += scratch[w];
+            all += scratch[w];
+        }
+        if (want >= off + upto - mine && want < off + upto) {
+            scratch[16] = b;
+            scratch[17] = off + upto - mine;
+        }
+        at += all;
+        if (want < at) break;
+    }
+    __syncthreads();
+    seq = (int)scratch[16];
+    before = scratch[17];
+    __syncthreads();
+}
+
+// Walks the tiles of a block's share.
+struct Walk {
+    int b, vh, tile, tiles, len;
+    __device__ __forceinline__ void next(const DecodeArgs &a) {
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++vh < a.vheads) return;
+        vh = 0;
+        do {   // the caller stops at its share's end, so there is a next sequence when this is used
+            ++b;
+            len = b < a.n ? decode_len(a, b) : kDecodeTile;
+        } while (len == 0);
+        tiles = (len + kDecodeTile - 1) / kDecodeTile;
+    }
+};
+
+template <typename T, int D, int GC> struct DecodeCfg {
+    static constexpr int kRowBytes = D * (int)sizeof(T);
+    static constexpr int kStageBytes = 2 * kWarpTokens * kRowBytes;   // keys and values of a warp's tokens
+    static constexpr int kStages = 3;
+    static constexpr int kRing = kDecodeWarps * kStages * kStageBytes;
+    static constexpr int kQ = GC * D * 4;
+    static constexpr int kP = kDecodeWarps * GC * kWarpTokens * 4;
+    static constexpr int kJoin = kDecodeWarps * GC * (D + 2) * 4;
+    static constexpr int kSmem = kRing + kQ + kP + kJoin + 160;
+};
+
+// Copies a warp's 16 tokens of the tile at `w` into its stage; returns a mask of the valid ones.
+template <typename T, int D>
+__device__ __forceinline__ uint32_t load_tokens(const DecodeArgs &a, const Walk &w, int warp, int lane, int hkv,
+                                                uint32_t stage) {
+    constexpr int CH = D * (int)sizeof(T) / 16;   // 16-byte chunks of a row
+    const int t0 = w.tile * kDecodeTile + warp * kWarpTokens;
+    // lanes 0-15 look up their token's page
+    const int tok = t0 + (lane & 15);
+    int page = -1;
+    if (tok < w.len) {
+        page = __ldg(a.cache.table + w.b * a.cache.row + (tok >> a.cache.page_log2));
+        if (page < 0 || page >= a.cache.num_pages) {
+            record_device_error(kDevErrBadPage);
+            page = -1;
+        }
+    }
+    const uint32_t valid = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+    const int in_page = (1 << a.cache.page_log2) - 1;
+#pragma unroll
+    for (int i = 0; i < kWarpTokens * CH / 32; ++i) {
+        const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
+        const int pg = __shfl_sync(0xffffffffu, page, r);
+        const int64_t slot = ((int64_t)hkv << a.cache.page_log2) + ((t0 + r) & in_page);
+        const T *kr = static_cast<const T *>(a.cache.k), *vr = static_cast<const T *>(a.cache.v);
+        if (pg >= 0) {
+            kr += pg * a.cache.k_stride + slot * D;
+            vr += pg * a.cache.v_stride + slot * D;
+        }
+        const uint32_t off = r * (CH * 16) + (((c & ~7) | ((c ^ r) & 7)) << 4);
+        cp_async16(stage + off, kr + (pg >= 0 ? c * (16 / (int)sizeof(T)) : 0), pg >= 0);
+        cp_async16(stage + kWarpTokens * CH * 16 + off, vr + (pg >= 0 ? c * (16 / (int)sizeof(T)) : 0), pg >= 0);
+    }
+    return valid;
+}
+
+// Channels [4 i, 4 i + 4) of a row staged by load_tokens.
+template <int D> __device__ __forceinline__ float4 staged4(const float *rows, int r, int i) {
+    constexpr int CH = D * 4 / 16;
+    const int c = i;
+    return *reinterpret_cast<const float4 *>(reinterpret_cast<const char *>(rows) + r * (CH * 16) +
+                                             (((c & ~7) | ((c ^ r) & 7)) << 4));
+}
+template <int D> __device__ __forceinline__ float4 staged4(const __nv_bfloat16 *rows, int r, int i) {
+    constexpr int CH = D * 2 / 16;
+    const int c = i >> 1;
+    const uint2 u = *reinterpret_cast<const uint2 *>(reinterpret_cast<const char *>(rows) + r * (CH * 16) +
+                                                     (((c & ~7) | ((c ^ r) & 7)) << 4) + (i & 1) * 8);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+
+template <typename T, int D, int GC>
+__global__ void __launch_bounds__(kDecodeWarps * 32, 1) attn_decode_kernel(const DecodeArgs a) {
+    using C = DecodeCfg<T, D, GC>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float *s_q = reinterpret_cast<float *>(smem + C::kRing);
+    float *s_join = s_q + GC * D + kDecodeWarps * GC * kWarpTokens;
+    int64_t *scratch = reinterpret_cast<int64_t *>(smem + C::kRing + C::kQ + C::kP + C::kJoin);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float *s_p = s_q + GC * D + warp * GC * kWarpTokens;
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kStages * C::kStageBytes;
+    const uint8_t *ring_ptr = smem + warp * C::kStages * C::kStageBytes;
+
+    // this block's share of the line of tiles
+    int64_t mine = 0;
+    for (int b = tid; b < a.n; b += blockDim.x) mine += decode_tiles(a, b);
+    const int64_t all = block_sum(mine, scratch) * a.vheads;
+    const int64_t first = all * blockIdx.x / a.blocks, last = all * (blockIdx.x + 1) / a.blocks;
+    if (first >= last) return;
+    int seq;
+    int64_t before;
+    find_sequence(a, first / a.vheads, scratch, seq, before);
+    Walk w;
+    w.b = seq;
+    w.len = decode_len(a, seq);
+    w.tiles = (w.len + kDecodeTile - 1) / kDecodeTile;
+    const int64_t in_seq = first - before * a.vheads;
+    w.vh = (int)(in_seq / w.tiles);
+    w.tile = (int)(in_seq % w.tiles);
+    Walk ahead = w;
+
+    const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv;
+    uint32_t valid[C::kStages];
+    int64_t issued = first;
+#pragma unroll
+    for (int s = 0; s < C::kStages; ++s) valid[s] = 0;
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) {
+        if (issued < last) {
+            valid[s] = load_tokens<T, D>(a, ahead, warp, lane, ahead.vh / chunks, ring + s * C::kStageBytes);
+            ahead.next(a);
+            ++issued;
+        }
+        cp_async_commit();
+    }
+
+    constexpr int CPL = D / 32;   // channels of a lane in the output
+    float m[GC], l[GC], o[GC][CPL];
+    const int row = lane & 15, half = lane >> 4;
+    bool starts_inside = w.tile != 0;   // the first pair began in an earlier block
+    bool fresh = true;
+    int st = 0;
+    for (int64_t i = first; i < last; ++i) {
+        const int hkv = w.vh / chunks, h0 = hkv * group + (w.vh % chunks) * GC;
+        const int nh = min(GC, hkv * group + group - h0);
+        if (fresh) {   // a new pair: its queries, scaled so that exp is 2^x
+            __syncthreads();
+            for (int e = tid; e < GC * D; e += blockDim.x) {
+                const int g = e / D;
+                s_q[e] = g < nh ? to_f32(static_cast<const T *>(a.q)[w.b * a.q_stride + (int64_t)h0 * D + e]) *
+                                      (a.scale * kLog2e)
+                                : 0.f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int g = 0; g < GC; ++g) {
+                m[g] = -CUDART_INF_F;
+                l[g] = 0.f;
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) o[g][c] = 0.f;
+            }
+            fresh = false;
+        }
+        // keep the ring full
+        {
+            const int into = (st + C::kStages - 1) % C::kStages;
+            uint32_t got = 0;
+            if (issued < last) {
+                got = load_tokens<T, D>(a, ahead, warp, lane, ahead.vh / chunks, ring + into * C::kStageBytes);
+                ahead.next(a);
+                ++issued;
+            }
+            cp_async_commit();
+#pragma unroll
+            for (int s = 0; s < C::kStages; ++s)
+                if (s == into) valid[s] = got;
+        }
+        cp_async_wait<C::kStages - 1>();
+        __syncwarp();
+        uint32_t ok = 0;
+#pragma unroll
+        for (int s = 0; s < C::kStages; ++s)
+            if (s == st) ok = valid[s];
+        const T *ks = reinterpret_cast<const T *>(ring_ptr + st * C::kStageBytes);
+        const T *vs = ks + kWarpTokens * D;
+
+        // scores: lane (row, half) sums half of the channels of one key
+        float s[GC];
+#pragma unroll
+        for (int g = 0; g < GC; ++g) s[g] = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+            const int at = half * (D / 8) + c;
+            const float4 kk = staged4<D>(ks, row, at);
+#pragma unroll
+            for (int g = 0; g < GC; ++g) {
+                const float4 qq = *reinterpret_cast<const float4 *>(s_q + g * D + 4 * at);
+                s[g] += qq.x * kk.x + qq.y * kk.y + qq.z * kk.z + qq.w * kk.w;
+            }
+        }
+        const bool live = (ok >> row) & 1;
+#pragma unroll
+        for (int g = 0; g < GC; ++g) {
+            float x = s[g] + __shfl_xor_sync(0xffffffffu, s[g], 16);
+            x = live ? x : -CUDART_INF_F;
+            float top = x;
+#pragma unroll
+            for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float mn = fmaxf(m[g], top), base = mn == -CUDART_INF_F ? 0.f : mn;
+            const float f = exp2f(m[g] - base), p = live ? exp2f(x - base) : 0.f;
+            m[g] = mn;
+            l[g] = l[g] * f + (half == 0 ? p : 0.f);   // a lane's own share of the sum
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) o[g][c] *= f;
+            if (half == 0) s_p[g * kWarpTokens + row] = p;
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int t = 0; t < kWarpTokens; ++t) {
+            const float4 x = staged4<D>(vs, t, lane * CPL / 4);
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int g = 0; g < GC; ++g) {
+                const float p = s_p[g * kWarpTokens + t];
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) o[g][c] += p * xs[CPL == 4 ? c : (lane & 1) * 2 + c];
+            }
+        }
+        __syncwarp();
+
+        st = (st + 1) % C::kStages;
+        const Walk cur = w;
+        if (i + 1 < last) w.next(a);
+        if (i + 1 == last || w.b != cur.b || w.vh != cur.vh) {
+            // the end of this block's part of a pair: join the warps
+            const bool ends_inside = cur.tile + 1 < cur.tiles;
+            const bool whole = !starts_inside && !ends_inside;
+            float *mine_j = s_join + warp * GC * (D + 2);
+#pragma unroll
+            for (int g = 0; g < GC; ++g) {
+                float sum = l[g];
+#pragma unroll
+                for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (lane == 0) {
+                    mine_j[g * (D + 2)] = m[g];
+                    mine_j[g * (D + 2) + 1] = sum;
+                }
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) mine_j[g * (D + 2) + 2 + lane * CPL + c] = o[g][c];
+            }
+            __syncthreads();
+            // the first pair of a share leaves its part in slot 0, the last in slot 1
+            float *part = a.part + ((int64_t)blockIdx.x * 2 + (starts_inside || i + 1 != last ? 0 : 1)) * GC * (D + 2);
+            for (int e = tid; e < nh * D; e += blockDim.x) {
+                const int g = e / D, c = e % D;
+                float top = -CUDART_INF_F;
+#pragma unroll
+                for (int k = 0; k < kDecodeWarps; ++k) top = fmaxf(top, s_join[(k * GC + g) * (D + 2)]);
+                const float base = top == -CUDART_INF_F ? 0.f : top;
+                float sum = 0.f, acc = 0.f;
+#pragma unroll
+                for (int k = 0; k < kDecodeWarps; ++k) {
+                    const float *j = s_join + (k * GC + g) * (D + 2);
+                    const float f = exp2f(j[0] - base);
+                    sum += f * j[1];
+                    acc += f * j[2 + c];
+                }
+                if (whole) {
+                    const int64_t h = (int64_t)cur.b * a.Hq + h0 + g;
+                    static_cast<T *>(a.out)[h * D + c] = from_f32<T>(sum > 0.f || sum != sum ? acc / sum : 0.f);
+                    if (c == 0 && a.lse)
+                        a.lse[h] = sum == 0.f ? -CUDART_INF_F : top * 0.69314718055994531f + logf(sum);
+                } else {
+                    part[g * (D + 2) + 2 + c] = acc;
+                    if (c == 0) {
+                        part[g * (D + 2)] = top;
+                        part[g * (D + 2) + 1] = sum;
+                    }
+                }
+            }
+            __syncthreads();
+            starts_inside = false;
+            fresh = true;
+        }
+    }
+    cp_async_wait<0>();
+}
+
+// Joins the parts of every pair that more than one block worked on, and writes the rows of sequences
+// without a token (zeros, lse -inf).  One block per (sequence, head group); thread c owns channel c.
+template <typename T, int D, int GC> __global__ void __launch_bounds__(128) attn_decode_join_kernel(const DecodeArgs a) {
+    __shared__ int64_t scratch[20];
+    const int tid = threadIdx.x, b = blockIdx.x / a.vheads, vh = blockIdx.x % a.vheads;
+    int64_t all = 0, before = 0;
+    for (int n = tid; n < a.n; n += blockDim.x) {
+        const int t = decode_tiles(a, n);
+        all += t;
+        if (n < b) before += t;
+    }
+    all = block_sum(all, scratch) * a.vheads;
+    before = block_sum(before, scratch) * a.vheads;
+    const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv, hkv = vh / chunks, h0 = hkv * group + (vh % chunks) * GC;
+    const int nh = min(GC, hkv * group + group - h0);
+    const int len = decode_len(a, b), tiles = decode_tiles(a, b);
+    if (tid == 0 && vh == 0 && __ldg(a.lens + b) > len) record_device_error(kDevErrBadPage);
+    T *out = static_cast<T *>(a.out) + ((int64_t)b * a.Hq + h0) * D;
+    if (tiles == 0) {
+        for (int e = tid; e < nh * D; e += blockDim.x) out[e] = from_f32<T>(0.f);
+        if (a.lse && tid < nh) a.lse[(int64_t)b * a.Hq + h0 + tid] = -CUDART_INF_F;
+        return;
+    }
+    const int64_t s0 = before + (int64_t)vh * tiles, s1 = s0 + tiles;
+    // blocks whose share [all c / blocks, all (c + 1) / blocks) meets [s0, s1)
+    int64_t c0 = s0 * a.blocks / all, c1 = (s1 - 1) * a.blocks / all;
+    while (all * (c0 + 1) / a.blocks <= s0) ++c0;
+    while (c0 > 0 && all * c0 / a.blocks > s0) --c0;
+    while (all * (c1 + 1) / a.blocks <= s1 - 1) ++c1;
+    while (c1 > 0 && all * c1 / a.blocks > s1 - 1) --c1;
+    if (c0 == c1) return;   // one block had it all and wrote the output
+    for (int e = tid; e < nh * D; e += blockDim.x) {
+        const int g = e / D, c = e % D;
+        float top = -CUDART_INF_F, sum = 0.f, acc = 0.f;
+        for (int64_t k = c0; k <= c1; ++k) {
+            // the pair is the block's first if it began at or before the share's begin
+            const int64_t from = all * k / a.blocks;
+            if (from >= all * (k + 1) / a.blocks) continue;   // an empty share
+            const int slot = s0 < from ? 0 : 1;
+            const float *p = a.part + ((k * 2 + slot) * GC + g) * (D + 2);
+            const float mk = p[0], mn = fmaxf(top, mk), base = mn == -CUDART_INF_F ? 0.f : mn;
+            const float f = exp2f(top - base), fk = exp2f(mk - base);
+            sum = sum * f + p[1] * fk;
+            acc = acc * f + p[2 + c] * fk;
+            top = mn;
+        }
+        out[g * D + c] = from_f32<T>(sum > 0.f || sum != sum ? acc / sum : 0.f);
+        if (c == 0 && a.lse)
+            a.lse[(int64_t)b * a.Hq + h0 + g] = sum == 0.f ? -CUDART_INF_F : top * 0.69314718055994531f + logf(sum);
+    }
+}
+
+// Query heads that a block takes together: the whole group up to 8, in equal parts above.
+inline int decode_group_chunk(int group) { return group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8; }
+
+inline int64_t decode_max_tiles(int n, int vheads, int64_t tokens) {
+    return (int64_t)n * vheads * ((tokens + kDecodeTile - 1) / kDecodeTile);
+}
+
+inline int decode_blocks(int n, int vheads, int64_t tokens, int sms) {
+    const int64_t t = decode_max_tiles(n, vheads, tokens);
+    return (int)(t < sms ? (t > 0 ? t : 1) : sms);
+}
+
+constexpr int kMaxDecodeBlocks = 1024;
+inline size_t decode_workspace_bytes(int group, int d) {
+    return (size_t)kMaxDecodeBlocks * 2 * decode_group_chunk(group) * (d + 2) * 4;
+}
+
+template <typename T, int D, int GC> cudaError_t launch_decode_g(DecodeArgs a, int sms, cudaStream_t st) {
+    using C = DecodeCfg<T, D, GC>;
+    auto kern = attn_decode_kernel<T, D, GC>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    a.vheads = a.Hkv * ((a.Hq / a.Hkv + GC - 1) / GC);
+    a.blocks = decode_blocks(a.n, a.vheads, (int64_t)a.cache.width << a.cache.page_log2, sms);
+    if (a.blocks > kMaxDecodeBlocks) a.blocks = kMaxDecodeBlocks;
+    kern<<<a.blocks, kDecodeWarps * 32, C::kSmem, st>>>(a);
+    attn_decode_join_kernel<T, D, GC><<<(unsigned)((int64_t)a.n * a.vheads), 128, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int D> cudaError_t launch_attn_decode(const DecodeArgs &a, int sms, cudaStream_t st) {
+    switch (decode_group_chunk(a.Hq / a.Hkv)) {
+        case 1: return launch_decode_g<T, D, 1>(a, sms, st);
+        case 2: return launch_decode_g<T, D, 2>(a, sms, st);
+        case 4: return launch_decode_g<T, D, 4>(a, sms, st);
+        default: return launch_decode_g<T, D, 8>(a, sms, st);
+    }
+}
+
+}  // namespace attn
+}  // namespace kda

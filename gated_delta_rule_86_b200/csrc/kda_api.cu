@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "../../include/kda.h"
+#include "attn_api.cuh"
 #include "kda_backward.cuh"
 #include "kda_chunk_tc.cuh"
 #include "kda_common.cuh"
@@ -134,11 +135,12 @@ const char *kda_status_string(kda_status s) {
         case KDA_ERR_UNSUPPORTED: return "KDA_ERR_UNSUPPORTED";
         case KDA_ERR_CUDA: return "KDA_ERR_CUDA";
         case KDA_ERR_TIMEOUT: return "KDA_ERR_TIMEOUT";
+        case KDA_ERR_BAD_PAGE: return "KDA_ERR_BAD_PAGE";
     }
     return "KDA_ERR_UNKNOWN";
 }
 
-const char *kda_version(void) { return "kda_b200 0.2.0 sm_100a"; }
+const char *kda_version(void) { return "kda_b200 0.3.0 sm_100a"; }
 
 kda_status kda_testing_set_chunk_fault(int32_t skip_item, uint32_t flag_wait_us) {
     if (skip_item < -1) return KDA_ERR_INVALID_ARG;

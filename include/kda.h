@@ -19,7 +19,10 @@
  * (kda_decode_step); the same from the raw projections (kda_chunk_fwd_fused,
  * kda_decode_step_fused); Gated DeltaNet and DeltaNet (gdn_chunk_fwd,
  * gdn_recurrent_fwd, gdn_decode_step); the gradient of the prefill
- * (kda_chunk_bwd); status helpers.
+ * (kda_chunk_bwd); softmax attention for the full-attention layers that hybrid
+ * models put between those (kda_attn_fwd and its gradient kda_attn_bwd for
+ * prompts, kda_kv_append and kda_attn_decode_step over a paged key-value
+ * cache); status helpers.
  *
  * Conventions for every call
  *  - All tensor pointers are DEVICE pointers owned by the caller; the library
@@ -55,7 +58,9 @@ typedef enum {
     KDA_ERR_INVALID_ARG = 1,   /* null pointer, bad shape, misaligned pointer, bad cu_seqlens size */
     KDA_ERR_UNSUPPORTED = 2,   /* valid but not implemented: head size, chunk size, dtype */
     KDA_ERR_CUDA = 3,          /* a CUDA runtime call or launch failed */
-    KDA_ERR_TIMEOUT = 4        /* a kernel gave up on a bounded wait (device error word) */
+    KDA_ERR_TIMEOUT = 4,       /* a kernel gave up on a bounded wait (device error word) */
+    KDA_ERR_BAD_PAGE = 5       /* a page table named no page of the pool, or a sequence does not fit
+                                  its row of the table (device error word) */
 } kda_status;
 
 typedef enum {
@@ -313,17 +318,133 @@ kda_status kda_chunk_bwd(const void *q, const void *k, const void *v, const void
 kda_status kda_chunk_bwd_workspace_size(int32_t N, int32_t H, int64_t total_tokens, int32_t d_k,
                                         int32_t d_v, int32_t chunk, size_t *bytes);
 
+/*
+ * Softmax attention.  The full-attention layers of a hybrid model (sections
+ * "Core Module Design" and on layer ratios of the pages: three KDA layers to
+ * one full-attention layer) in the forms that training, prompts and decoding
+ * need.  Query heads come in Hkv groups of Hq / Hkv that share a head of keys
+ * and values (query head h reads head h / (Hq / Hkv)); Hq must be a multiple of Hkv.
+ * Supported: d in {64, 128}, bf16 or fp32 (both for every tensor of a call but
+ * the fp32 lse).  Token strides (q_stride, k_stride, v_stride) are in elements,
+ * 0 meaning dense (heads * d); they let q, k and v be slices of one projection,
+ * and must keep rows 16-byte aligned.  Outputs are dense.  Softmax statistics and sums are fp32.
+ *
+ * kda_attn_fwd -- attention over whole prompts.
+ *
+ *     O = softmax(scale Q K^T + mask) V,   lse_i = log sum_j exp(scale q_i . k_j)
+ *
+ *   q             : [B, Tq, Hq, d];  k, v : [B, Tk, Hkv, d]
+ *   cu_seqlens_q  : NULL, or int32 [num_seqs + 1] (device) with B == 1: packed
+ *                   sequences, ascending, cu_seqlens_q[0] == 0 and the last at
+ *                   most Tq (not checked; the kernels keep inside the tensors).
+ *                   Rows of out and lse behind the last sequence are left as
+ *                   they were.  Empty sequences are allowed.
+ *   cu_seqlens_k  : the keys' offsets, or NULL for those of the queries (Tk == Tq).
+ *   causal        : non-zero: query i of a sequence with nq queries and nk keys
+ *                   sees keys j <= i + nk - nq (the last query sees all keys); a
+ *                   query that sees none gets out = 0, lse = -inf.
+ *   scale         : finite and positive.
+ *   out           : [B, Tq, Hq, d];  lse : fp32 [B, Hq, Tq], or NULL.
+ * A sequence never sees another's keys, whatever they hold (NaN included).
+ * Inside a sequence, keys and values that the causal mask hides must be finite
+ * for bf16: a hidden value enters the tensor cores' sums with weight zero.
+ */
+kda_status kda_attn_fwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                        int64_t v_stride, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                        int32_t num_seqs, int32_t B, int32_t Tq, int32_t Tk, int32_t Hq, int32_t Hkv,
+                        int32_t d, int32_t causal, float scale, kda_dtype dtype, void *out, float *lse,
+                        void *stream);
+
+/*
+ * kda_attn_bwd -- gradient of kda_attn_fwd.
+ *
+ *     P = exp(scale Q K^T - lse),  delta = rowsum(dO o O),  dS = P o (dO V^T - delta),
+ *     dV = P^T dO,   dK = scale dS^T Q,   dQ = scale dS K
+ * with dK and dV summed over the query heads of a group.  Takes the forward's
+ * inputs, its out and lse, and d_out [B, Tq, Hq, d] (dense); writes dq [B, Tq,
+ * Hq, d], dk and dv [B, Tk, Hkv, d] in the inputs' type.  Rows behind the last
+ * packed sequence get zero gradients.  The order of every sum is fixed: the
+ * same call gives the same bits.  workspace: kda_attn_bwd_workspace_size bytes.
+ */
+kda_status kda_attn_bwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                        int64_t v_stride, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                        int32_t num_seqs, int32_t B, int32_t Tq, int32_t Tk, int32_t Hq, int32_t Hkv,
+                        int32_t d, int32_t causal, float scale, kda_dtype dtype, const void *out,
+                        const float *lse, const void *d_out, void *dq, void *dk, void *dv,
+                        void *workspace, size_t workspace_bytes, void *stream);
+kda_status kda_attn_bwd_workspace_size(int32_t B, int32_t Tq, int32_t Hq, size_t *bytes);
+
+/*
+ * The paged cache: k_cache and v_cache are [num_pages, Hkv, page_size, d], pages
+ * k_page_stride / v_page_stride elements apart (0: dense), page_size a power of
+ * two (KDA_ERR_UNSUPPORTED otherwise).  page_table is int32 [sequences,
+ * table_width], rows table_stride entries apart (0: table_width): token p of
+ * sequence n lies in page page_table[n][p / page_size], slot p % page_size.
+ *
+ * kda_kv_append -- writes new keys and values into the cache, rotating keys (and
+ * queries) by their positions on the way.
+ *
+ *   q           : [B, T, Hq, d] or NULL;  k, v : [B, T, Hkv, d]
+ *   cu_seqlens  : NULL, or int32 [num_seqs + 1] with B == 1 (packed sequences).
+ *   cache_lens  : int32 [sequences]: tokens that the cache holds of each before
+ *                 the call.  Token j gets position cache_lens[n] + j.  A negative
+ *                 entry marks an unused row: nothing of it is read or written.
+ *                 Not changed by the call (the layers of a model share it).
+ *   inv_freq    : fp32 [rotary_dim / 2] (device); rotary_dim 0: no rotation.  The
+ *                 first rotary_dim channels turn in pairs (i, i + rotary_dim / 2),
+ *                 or (2i, 2i + 1) when interleaved, by position * inv_freq[i], an
+ *                 angle formed in 64 bits.  rotary_dim must be a multiple of 16.
+ *   q_out       : [B, T, Hq, d] (dense; may be q itself where q is dense), given
+ *                 exactly when q is.
+ *   k_out       : [B, T, Hkv, d] (dense) or NULL: the rotated keys once more, for the prompt's attention.
+ * A token whose page is not in [0, num_pages), or beyond its row of the table,
+ * is not written, and the device error word becomes KDA_ERR_BAD_PAGE.  Rows
+ * behind the last packed sequence are not touched.  Two tokens of one call must
+ * not share a slot.
+ */
+kda_status kda_kv_append(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                         int64_t v_stride, const float *inv_freq, int32_t rotary_dim, int32_t interleaved,
+                         const int32_t *cu_seqlens, int32_t num_seqs, int32_t B, int32_t T, int32_t Hq,
+                         int32_t Hkv, int32_t d, kda_dtype dtype, const int32_t *cache_lens,
+                         const int32_t *page_table, int64_t table_stride, int32_t table_width,
+                         void *k_cache, void *v_cache, int64_t k_page_stride, int64_t v_page_stride,
+                         int32_t num_pages, int32_t page_size, void *q_out, void *k_out, void *stream);
+
+/*
+ * kda_attn_decode_step -- attention of one new token per sequence over the cache.
+ *
+ *   q         : [B, Hq, d], rows q_stride elements apart (0: dense)
+ *   seq_lens  : int32 [B]: tokens of each sequence in the cache, the new one's
+ *               key among them.  A sequence without tokens (<= 0) gets out = 0,
+ *               lse = -inf.  One longer than its row of the table is cut there,
+ *               and tokens on a page outside the pool are left out; either makes
+ *               the device error word KDA_ERR_BAD_PAGE.
+ *   out       : [B, Hq, d];  lse : fp32 [B, Hq] or NULL.
+ *   workspace : kda_attn_decode_workspace_size bytes, needing no initialisation.
+ * Slots past a sequence's end are never read.  The order of every sum is fixed
+ * by the lengths: the same call gives the same bits.
+ */
+kda_status kda_attn_decode_step(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                                int64_t k_page_stride, int64_t v_page_stride, int32_t num_pages,
+                                int32_t page_size, const int32_t *page_table, int64_t table_stride,
+                                int32_t table_width, const int32_t *seq_lens, int32_t B, int32_t Hq,
+                                int32_t Hkv, int32_t d, float scale, kda_dtype dtype, void *out,
+                                float *lse, void *workspace, size_t workspace_bytes, void *stream);
+kda_status kda_attn_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype dtype,
+                                          size_t *bytes);
+
 /* Human-readable name of a status (static string, never NULL). */
 const char *kda_status_string(kda_status s);
 
 /*
  * Synchronises `stream`, then returns and clears the device-side error word
- * of the current device: KDA_OK, or KDA_ERR_TIMEOUT if a kernel gave up on a
- * bounded wait since the last call.  KDA_ERR_CUDA if the sync or read failed.
+ * of the current device: KDA_OK, KDA_ERR_TIMEOUT if a kernel gave up on a
+ * bounded wait since the last call, or KDA_ERR_BAD_PAGE if one met a page or
+ * length outside the cache (the larger code if both).  KDA_ERR_CUDA if the sync or read failed.
  */
 kda_status kda_get_last_device_error(void *stream);
 
-/* Library version string, e.g. "kda_b200 0.2.0 sm_100a". */
+/* Library version string, e.g. "kda_b200 0.3.0 sm_100a". */
 const char *kda_version(void);
 
 /*
