@@ -8,6 +8,7 @@
 #include "attn_append.cuh"
 #include "attn_decode.cuh"
 #include "attn_prompt.cuh"
+#include "attn_prompt_tc.cuh"
 #include "kda_chunk_tc.cuh"
 
 namespace kda {
@@ -239,7 +240,7 @@ kda_status kda_attn_fwd(const void *q, const void *k, const void *v, int64_t q_s
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == KDA_F32)
         return status_of(d == 64 ? launch_prompt<float, 64>(a, st) : launch_prompt<float, 128>(a, st));
-    return status_of(d == 64 ? launch_prompt<__nv_bfloat16, 64>(a, st) : launch_prompt<__nv_bfloat16, 128>(a, st));
+    return status_of(d == 64 ? launch_prompt_tc<64>(a, st) : launch_prompt_tc<128>(a, st));
 }
 
 kda_status kda_attn_bwd_workspace_size(int32_t B, int32_t Tq, int32_t Hq, size_t *bytes) {
