@@ -7,6 +7,7 @@
 #include "../../include/kda.h"
 #include "attn_append.cuh"
 #include "attn_decode.cuh"
+#include "attn_grad_tc.cuh"
 #include "attn_prompt.cuh"
 #include "attn_prompt_tc.cuh"
 #include "kda_chunk_tc.cuh"
@@ -275,8 +276,7 @@ kda_status kda_attn_bwd(const void *q, const void *k, const void *v, int64_t q_s
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == KDA_F32)
         return status_of(d == 64 ? launch_prompt_grad<float, 64>(a, st) : launch_prompt_grad<float, 128>(a, st));
-    return status_of(d == 64 ? launch_prompt_grad<__nv_bfloat16, 64>(a, st)
-                             : launch_prompt_grad<__nv_bfloat16, 128>(a, st));
+    return status_of(d == 64 ? launch_prompt_grad_tc<64>(a, st) : launch_prompt_grad_tc<128>(a, st));
 }
 
 }  // extern "C"
