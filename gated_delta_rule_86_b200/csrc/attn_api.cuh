@@ -6,7 +6,7 @@
 
 #include "../../include/kda.h"
 #include "attn_append.cuh"
-#include "attn_decode.cuh"
+#include "attn_decode_mma.cuh"
 #include "attn_grad_tc.cuh"
 #include "attn_prompt.cuh"
 #include "attn_prompt_tc.cuh"
@@ -178,7 +178,7 @@ kda_status kda_attn_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, in
     *bytes = 0;
     const kda_status s = check_heads(Hq, Hkv, d, dtype);
     if (s != KDA_OK) return s;
-    *bytes = decode_workspace_bytes(Hq / Hkv, d);
+    *bytes = decode_workspace_bytes(Hq / Hkv, d, dtype == KDA_BF16);
     return KDA_OK;
 }
 
@@ -203,10 +203,10 @@ kda_status kda_attn_decode_step(const void *q, int64_t q_stride, const void *k_c
         KDA_OK)
         return s;
     if (heads != KDA_OK) return heads;
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < decode_workspace_bytes(Hq / Hkv, d))
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < decode_workspace_bytes(Hq / Hkv, d, dtype == KDA_BF16))
         return KDA_ERR_INVALID_ARG;
     if ((int64_t)B * Hq > 0x7fffffff) return KDA_ERR_UNSUPPORTED;
-    if (((int64_t)table_width << a.cache.page_log2) > 0x7fffffff - kDecodeTile) return KDA_ERR_UNSUPPORTED;
+    if (((int64_t)table_width << a.cache.page_log2) > 0x7fffffff - 1024) return KDA_ERR_UNSUPPORTED;
     a.q = q;
     a.q_stride = q_stride;
     a.lens = seq_lens;
@@ -221,9 +221,8 @@ kda_status kda_attn_decode_step(const void *q, int64_t q_stride, const void *k_c
     if (sms < 1) return KDA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == KDA_F32)
-        return status_of(d == 64 ? launch_attn_decode<float, 64>(a, sms, st) : launch_attn_decode<float, 128>(a, sms, st));
-    return status_of(d == 64 ? launch_attn_decode<__nv_bfloat16, 64>(a, sms, st)
-                             : launch_attn_decode<__nv_bfloat16, 128>(a, sms, st));
+        return status_of(d == 64 ? launch_attn_decode_f32<64>(a, sms, st) : launch_attn_decode_f32<128>(a, sms, st));
+    return status_of(d == 64 ? launch_attn_decode_bf16<64>(a, sms, st) : launch_attn_decode_bf16<128>(a, sms, st));
 }
 
 kda_status kda_attn_fwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,

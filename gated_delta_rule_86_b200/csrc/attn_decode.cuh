@@ -20,9 +20,7 @@
 namespace kda {
 namespace attn {
 
-constexpr int kDecodeWarps = 4;
-constexpr int kWarpTokens = 16;
-constexpr int kDecodeTile = kDecodeWarps * kWarpTokens;
+constexpr int kWarpTokens = 16;   // of a tile, per warp
 
 struct DecodeArgs {
     const void *q;
@@ -51,8 +49,8 @@ __device__ __forceinline__ int decode_len(const DecodeArgs &a, int b) {
     const int64_t most = (int64_t)a.cache.width << a.cache.page_log2;
     return (int)min((int64_t)max(__ldg(a.lens + b), 0), most);
 }
-__device__ __forceinline__ int decode_tiles(const DecodeArgs &a, int b) {
-    return (decode_len(a, b) + kDecodeTile - 1) / kDecodeTile;
+template <int TILE> __device__ __forceinline__ int decode_tiles(const DecodeArgs &a, int b) {
+    return (decode_len(a, b) + TILE - 1) / TILE;
 }
 
 // Where the line of tiles stands before sequence b_stop, and (out) its whole length, in tiles of one
@@ -70,13 +68,14 @@ __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *scratch) {
 }
 
 // First sequence whose tiles reach beyond `want` (in tiles of one head group), and the tiles before it.
+template <int TILE>
 __device__ __forceinline__ void find_sequence(const DecodeArgs &a, int64_t want, int64_t *scratch, int &seq,
                                               int64_t &before) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     int64_t at = 0;
     for (int base = 0; base < a.n; base += blockDim.x) {
         const int b = base + threadIdx.x;
-        const int64_t mine = b < a.n ? decode_tiles(a, b) : 0;
+        const int64_t mine = b < a.n ? decode_tiles<TILE>(a, b) : 0;
         int64_t upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -104,9 +103,27 @@ __device__ __forceinline__ void find_sequence(const DecodeArgs &a, int64_t want,
     __syncthreads();
 }
 
-// Walks the tiles of a block's share.
-struct Walk {
+// Walks the tiles of a block's share of the line.
+template <int TILE> struct Walk {
     int b, vh, tile, tiles, len;
+    int64_t first, last;   // the share
+    // Works the share out from the lengths; false if it is empty.  Every thread of the block.
+    __device__ __forceinline__ bool start(const DecodeArgs &a, int64_t *scratch) {
+        int64_t mine = 0;
+        for (int n = threadIdx.x; n < a.n; n += blockDim.x) mine += decode_tiles<TILE>(a, n);
+        const int64_t all = block_sum(mine, scratch) * a.vheads;
+        first = all * blockIdx.x / a.blocks;
+        last = all * (blockIdx.x + 1) / a.blocks;
+        if (first >= last) return false;
+        int64_t before;
+        find_sequence<TILE>(a, first / a.vheads, scratch, b, before);
+        len = decode_len(a, b);
+        tiles = (len + TILE - 1) / TILE;
+        const int64_t in_seq = first - before * a.vheads;
+        vh = (int)(in_seq / tiles);
+        tile = (int)(in_seq % tiles);
+        return true;
+    }
     __device__ __forceinline__ void next(const DecodeArgs &a) {
         if (++tile < tiles) return;
         tile = 0;
@@ -114,9 +131,9 @@ struct Walk {
         vh = 0;
         do {   // the caller stops at its share's end, so there is a next sequence when this is used
             ++b;
-            len = b < a.n ? decode_len(a, b) : kDecodeTile;
+            len = b < a.n ? decode_len(a, b) : TILE;
         } while (len == 0);
-        tiles = (len + kDecodeTile - 1) / kDecodeTile;
+        tiles = (len + TILE - 1) / TILE;
     }
 };
 
@@ -124,6 +141,8 @@ template <typename T, int D, int GC> struct DecodeCfg {
     static constexpr int kRowBytes = D * (int)sizeof(T);
     static constexpr int kStageBytes = 2 * kWarpTokens * kRowBytes;   // keys and values of a warp's tokens
     static constexpr int kStages = 3;
+    static constexpr int kDecodeWarps = 4;
+    static constexpr int kTile = kDecodeWarps * kWarpTokens;
     static constexpr int kRing = kDecodeWarps * kStages * kStageBytes;
     static constexpr int kQ = GC * D * 4;
     static constexpr int kP = kDecodeWarps * GC * kWarpTokens * 4;
@@ -132,11 +151,11 @@ template <typename T, int D, int GC> struct DecodeCfg {
 };
 
 // Copies a warp's 16 tokens of the tile at `w` into its stage; returns a mask of the valid ones.
-template <typename T, int D>
-__device__ __forceinline__ uint32_t load_tokens(const DecodeArgs &a, const Walk &w, int warp, int lane, int hkv,
+template <typename T, int D, int TILE>
+__device__ __forceinline__ uint32_t load_tokens(const DecodeArgs &a, const Walk<TILE> &w, int warp, int lane, int hkv,
                                                 uint32_t stage) {
     constexpr int CH = D * (int)sizeof(T) / 16;   // 16-byte chunks of a row
-    const int t0 = w.tile * kDecodeTile + warp * kWarpTokens;
+    const int t0 = w.tile * TILE + warp * kWarpTokens;
     // lanes 0-15 look up their token's page
     const int tok = t0 + (lane & 15);
     int page = -1;
@@ -183,8 +202,9 @@ template <int D> __device__ __forceinline__ float4 staged4(const __nv_bfloat16 *
 }
 
 template <typename T, int D, int GC>
-__global__ void __launch_bounds__(kDecodeWarps * 32, 1) attn_decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) attn_decode_kernel(const DecodeArgs a) {
     using C = DecodeCfg<T, D, GC>;
+    constexpr int kDecodeWarps = C::kDecodeWarps;
     extern __shared__ __align__(1024) uint8_t smem[];
     float *s_q = reinterpret_cast<float *>(smem + C::kRing);
     float *s_join = s_q + GC * D + kDecodeWarps * GC * kWarpTokens;
@@ -195,23 +215,11 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1) attn_decode_kernel(const
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kStages * C::kStageBytes;
     const uint8_t *ring_ptr = smem + warp * C::kStages * C::kStageBytes;
 
-    // this block's share of the line of tiles
-    int64_t mine = 0;
-    for (int b = tid; b < a.n; b += blockDim.x) mine += decode_tiles(a, b);
-    const int64_t all = block_sum(mine, scratch) * a.vheads;
-    const int64_t first = all * blockIdx.x / a.blocks, last = all * (blockIdx.x + 1) / a.blocks;
-    if (first >= last) return;
-    int seq;
-    int64_t before;
-    find_sequence(a, first / a.vheads, scratch, seq, before);
-    Walk w;
-    w.b = seq;
-    w.len = decode_len(a, seq);
-    w.tiles = (w.len + kDecodeTile - 1) / kDecodeTile;
-    const int64_t in_seq = first - before * a.vheads;
-    w.vh = (int)(in_seq / w.tiles);
-    w.tile = (int)(in_seq % w.tiles);
-    Walk ahead = w;
+    asm volatile("griddepcontrol.launch_dependents;");   // the join may take its place; it waits for this grid's end
+    Walk<C::kTile> w;
+    if (!w.start(a, scratch)) return;
+    const int64_t first = w.first, last = w.last;
+    Walk<C::kTile> ahead = w;
 
     const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv;
     uint32_t valid[C::kStages];
@@ -221,7 +229,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1) attn_decode_kernel(const
 #pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s) {
         if (issued < last) {
-            valid[s] = load_tokens<T, D>(a, ahead, warp, lane, ahead.vh / chunks, ring + s * C::kStageBytes);
+            valid[s] = load_tokens<T, D, C::kTile>(a, ahead, warp, lane, ahead.vh / chunks, ring + s * C::kStageBytes);
             ahead.next(a);
             ++issued;
         }
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1) attn_decode_kernel(const
             const int into = (st + C::kStages - 1) % C::kStages;
             uint32_t got = 0;
             if (issued < last) {
-                got = load_tokens<T, D>(a, ahead, warp, lane, ahead.vh / chunks, ring + into * C::kStageBytes);
+                got = load_tokens<T, D, C::kTile>(a, ahead, warp, lane, ahead.vh / chunks, ring + into * C::kStageBytes);
                 ahead.next(a);
                 ++issued;
             }
@@ -323,7 +331,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1) attn_decode_kernel(const
         __syncwarp();
 
         st = (st + 1) % C::kStages;
-        const Walk cur = w;
+        const Walk<C::kTile> cur = w;
         if (i + 1 < last) w.next(a);
         if (i + 1 == last || w.b != cur.b || w.vh != cur.vh) {
             // the end of this block's part of a pair: join the warps
@@ -382,20 +390,22 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1) attn_decode_kernel(const
 
 // Joins the parts of every pair that more than one block worked on, and writes the rows of sequences
 // without a token (zeros, lse -inf).  One block per (sequence, head group); thread c owns channel c.
-template <typename T, int D, int GC> __global__ void __launch_bounds__(128) attn_decode_join_kernel(const DecodeArgs a) {
+template <typename T, int D, int GC, int TILE>
+__global__ void __launch_bounds__(128) attn_decode_join_kernel(const DecodeArgs a) {
     __shared__ int64_t scratch[20];
     const int tid = threadIdx.x, b = blockIdx.x / a.vheads, vh = blockIdx.x % a.vheads;
     int64_t all = 0, before = 0;
     for (int n = tid; n < a.n; n += blockDim.x) {
-        const int t = decode_tiles(a, n);
+        const int t = decode_tiles<TILE>(a, n);
         all += t;
         if (n < b) before += t;
     }
     all = block_sum(all, scratch) * a.vheads;
     before = block_sum(before, scratch) * a.vheads;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the main kernel's parts, from here on
     const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv, hkv = vh / chunks, h0 = hkv * group + (vh % chunks) * GC;
     const int nh = min(GC, hkv * group + group - h0);
-    const int len = decode_len(a, b), tiles = decode_tiles(a, b);
+    const int len = decode_len(a, b), tiles = decode_tiles<TILE>(a, b);
     if (tid == 0 && vh == 0 && __ldg(a.lens + b) > len) record_device_error(kDevErrBadPage);
     T *out = static_cast<T *>(a.out) + ((int64_t)b * a.Hq + h0) * D;
     if (tiles == 0) {
@@ -432,43 +442,31 @@ template <typename T, int D, int GC> __global__ void __launch_bounds__(128) attn
     }
 }
 
-// Query heads that a block takes together: the whole group up to 8, in equal parts above.
-inline int decode_group_chunk(int group) { return group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8; }
-
-inline int64_t decode_max_tiles(int n, int vheads, int64_t tokens) {
-    return (int64_t)n * vheads * ((tokens + kDecodeTile - 1) / kDecodeTile);
-}
-
-inline int decode_blocks(int n, int vheads, int64_t tokens, int sms) {
-    const int64_t t = decode_max_tiles(n, vheads, tokens);
-    return (int)(t < sms ? (t > 0 ? t : 1) : sms);
+// Launches a kernel that may start while the one before it in the stream still runs, and waits for it
+// itself (griddepcontrol.wait).
+template <typename... A, typename... B>
+cudaError_t launch_behind(void (*kern)(A...), unsigned grid, int threads, size_t smem, cudaStream_t st, const B &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 constexpr int kMaxDecodeBlocks = 1024;
-inline size_t decode_workspace_bytes(int group, int d) {
-    return (size_t)kMaxDecodeBlocks * 2 * decode_group_chunk(group) * (d + 2) * 4;
-}
 
-template <typename T, int D, int GC> cudaError_t launch_decode_g(DecodeArgs a, int sms, cudaStream_t st) {
-    using C = DecodeCfg<T, D, GC>;
-    auto kern = attn_decode_kernel<T, D, GC>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    a.vheads = a.Hkv * ((a.Hq / a.Hkv + GC - 1) / GC);
-    a.blocks = decode_blocks(a.n, a.vheads, (int64_t)a.cache.width << a.cache.page_log2, sms);
-    if (a.blocks > kMaxDecodeBlocks) a.blocks = kMaxDecodeBlocks;
-    kern<<<a.blocks, kDecodeWarps * 32, C::kSmem, st>>>(a);
-    attn_decode_join_kernel<T, D, GC><<<(unsigned)((int64_t)a.n * a.vheads), 128, 0, st>>>(a);
-    return cudaGetLastError();
-}
-
-template <typename T, int D> cudaError_t launch_attn_decode(const DecodeArgs &a, int sms, cudaStream_t st) {
-    switch (decode_group_chunk(a.Hq / a.Hkv)) {
-        case 1: return launch_decode_g<T, D, 1>(a, sms, st);
-        case 2: return launch_decode_g<T, D, 2>(a, sms, st);
-        case 4: return launch_decode_g<T, D, 4>(a, sms, st);
-        default: return launch_decode_g<T, D, 8>(a, sms, st);
-    }
+// Blocks of the main kernel: one per SM, no more than there can be tiles.
+inline int decode_blocks(const DecodeArgs &a, int tile, int sms) {
+    const int64_t tokens = (int64_t)a.cache.width << a.cache.page_log2;
+    const int64_t t = (int64_t)a.n * a.vheads * ((tokens + tile - 1) / tile);
+    const int most = sms < kMaxDecodeBlocks ? sms : kMaxDecodeBlocks;
+    return (int)(t < most ? t : most);
 }
 
 }  // namespace attn

@@ -1,0 +1,312 @@
+// attn_decode_mma.cuh -- the decode step's block for bf16, with the products on warp-level matrix
+// instructions, and the launch of both types.
+//
+// The schedule is that of attn_decode.cuh; here a block has 8 warps and a tile 128 tokens.  A head's
+// cache is read once for all query heads of its group, which at 8 heads asks for 8 multiplications per
+// loaded value and product: more than the FMA units give at the memory's pace, and little for m16n8k16
+// instructions.  Rows are the group's heads (up to 16), columns the warp's 16 tokens:
+//     S (16 x 16) = Q K^T      K straight from the staged rows
+//     O (16 x d) += P V        P from S's own registers, rounded to bf16, the operand type of V
+// tcgen05 would want 64 or 128 rows and its operands through Tensor Memory for the same few products;
+// the kernel is bound by the cache's bytes, not by these.
+#pragma once
+
+#include "attn_decode.cuh"
+
+namespace kda {
+namespace attn {
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D, int GC> struct DecodeMmaCfg {
+    static constexpr int kWarps = 8;
+    static constexpr int kTile = kWarps * kWarpTokens;
+    static constexpr int kRowBytes = D * 2;
+    static constexpr int kStageBytes = 2 * kWarpTokens * kRowBytes;
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kRing = kWarps * kStages * kStageBytes;
+    static constexpr int kJoinRows = 64;   // (warp, head) results that the join buffer holds at once
+    static constexpr int kPitch = D + 4;   // of a result: o, then m and the sum
+    static constexpr int kJoin = kJoinRows * kPitch * 4;
+    static constexpr int kSmem = kRing + kJoin + 160;
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+template <int D, int GC>
+__global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_decode_mma_kernel(const DecodeArgs a) {
+    using C = DecodeMmaCfg<D, GC>;
+    constexpr int CH = C::kRowBytes / 16;
+    constexpr int kShare = (GC * D + 255) / 256;   // of a pair's results, per thread, in the join
+    constexpr bool kBoth = GC > 8;   // rows 8-15 hold heads too
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float *s_join = reinterpret_cast<float *>(smem + C::kRing);
+    int64_t *scratch = reinterpret_cast<int64_t *>(smem + C::kRing + C::kJoin);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int gr = lane >> 2, gc = lane & 3;   // a fragment's row and column pair
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kStages * C::kStageBytes;
+
+    asm volatile("griddepcontrol.launch_dependents;");   // the join may take its place; it waits for this grid's end
+    Walk<C::kTile> w;
+    if (!w.start(a, scratch)) return;
+    const int64_t last = w.last;
+    Walk<C::kTile> ahead = w;
+    const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv;
+    uint32_t held[C::kStages];   // which of a stage's tokens there are
+#pragma unroll
+    for (int s = 0; s < C::kStages; ++s) held[s] = 0;
+    int64_t issued = w.first;
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) {
+        if (issued < last) {
+            held[s] = load_tokens<__nv_bfloat16, D, C::kTile>(a, ahead, warp, lane, ahead.vh / chunks, ring + s * C::kStageBytes);
+            ahead.next(a);
+            ++issued;
+        }
+        cp_async_commit();
+    }
+
+    // this lane's addresses inside a stage: ldmatrix rows
+    const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;   // K: tokens 0-7 | 8-15, chunk 0 | 1
+    const int vrow = lane & 15, vch = lane >> 4;                               // V: tokens 0-15, chunk 0 | 1
+    uint32_t qf[D / 16][4];
+    float o[D / 8][4];
+    float m[2], l[2];
+    const float sc = a.scale * kLog2e;
+    bool starts_inside = w.tile != 0, fresh = true;
+    int st = 0;
+    for (int64_t i = w.first; i < last; ++i) {
+        const int hkv = w.vh / chunks, h0 = hkv * group + (w.vh % chunks) * GC;
+        const int nh = min(GC, hkv * group + group - h0);
+        if (fresh) {
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                                   w.b * a.q_stride + (int64_t)h0 * D);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const int c = kk * 8 + gc;
+                qf[kk][0] = gr < nh ? __ldg(q + gr * (D / 2) + c) : 0u;
+                qf[kk][2] = gr < nh ? __ldg(q + gr * (D / 2) + c + 4) : 0u;
+                qf[kk][1] = kBoth && gr + 8 < nh ? __ldg(q + (gr + 8) * (D / 2) + c) : 0u;
+                qf[kk][3] = kBoth && gr + 8 < nh ? __ldg(q + (gr + 8) * (D / 2) + c + 4) : 0u;
+            }
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+            m[0] = m[1] = -CUDART_INF_F;
+            l[0] = l[1] = 0.f;
+            fresh = false;
+        }
+        {
+            uint32_t got = 0;
+            const int into = st == 0 ? C::kStages - 1 : st - 1;
+            if (issued < last) {
+                got = load_tokens<__nv_bfloat16, D, C::kTile>(a, ahead, warp, lane, ahead.vh / chunks,
+                                                              ring + into * C::kStageBytes);
+                ahead.next(a);
+                ++issued;
+            }
+            cp_async_commit();
+#pragma unroll
+            for (int s = 0; s < C::kStages; ++s)
+                if (s == into) held[s] = got;
+        }
+        cp_async_wait<C::kStages - 1>();
+        __syncwarp();
+        uint32_t ok = 0;
+#pragma unroll
+        for (int s = 0; s < C::kStages; ++s)
+            if (s == st) ok = held[s];
+        if (ok) {   // a warp's share of the tile may be empty
+            const uint32_t ks = ring + st * C::kStageBytes, vs = ks + kWarpTokens * C::kRowBytes;
+            float s0[4] = {}, s1[4] = {};   // tokens 0-7, 8-15
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint32_t b[4];
+                const int c = kk * 2 + kch;
+                ldsm4(b, ks + krow * (CH * 16) + (((c & ~7) | ((c ^ krow) & 7)) << 4));
+                mma_bf16(s0, qf[kk], b[0], b[1]);
+                mma_bf16(s1, qf[kk], b[2], b[3]);
+            }
+            uint32_t p[4] = {0u, 0u, 0u, 0u};
+            float f[2] = {1.f, 1.f};
+            bool any = false;
+#pragma unroll
+            for (int y = 0; y < (kBoth ? 2 : 1); ++y) {
+                float x[4] = {s0[2 * y], s0[2 * y + 1], s1[2 * y], s1[2 * y + 1]};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = (ok >> (2 * gc + (e & 1) + (e >> 1) * 8)) & 1 ? x[e] * sc : -CUDART_INF_F;
+                float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // the maximum in use follows the true one when it is 2^8 behind: weights up to 2^8 are as
+                // exact, and the accumulators are rescaled rarely
+                if (top - m[y] > 8.f) {
+                    f[y] = ex2_approx(m[y] - top);
+                    m[y] = top;
+                    any = true;
+                }
+                const float base = m[y] == -CUDART_INF_F ? 0.f : m[y];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = ex2_approx(x[e] - base);
+                l[y] = l[y] * f[y] + ((x[0] + x[1]) + (x[2] + x[3]));
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+                p[y] = *reinterpret_cast<const uint32_t *>(&lo);
+                p[2 + y] = *reinterpret_cast<const uint32_t *>(&hi);
+            }
+            if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    o[c][0] *= f[0];
+                    o[c][1] *= f[0];
+                    if (kBoth) {
+                        o[c][2] *= f[1];
+                        o[c][3] *= f[1];
+                    }
+                }
+            }
+#pragma unroll
+            for (int c2 = 0; c2 < D / 16; ++c2) {
+                uint32_t b[4];
+                const int c = c2 * 2 + vch;
+                ldsm4_t(b, vs + vrow * (CH * 16) + (((c & ~7) | ((c ^ vrow) & 7)) << 4));
+                mma_bf16(o[2 * c2], p, b[0], b[1]);
+                mma_bf16(o[2 * c2 + 1], p, b[2], b[3]);
+            }
+        }
+        __syncwarp();   // the stage is read before it is filled again
+        st = st + 1 == C::kStages ? 0 : st + 1;
+
+        const Walk<C::kTile> cur = w;
+        if (i + 1 < last) w.next(a);
+        if (i + 1 == last || w.b != cur.b || w.vh != cur.vh) {
+            const bool whole = !starts_inside && cur.tile + 1 == cur.tiles;
+            // the warps' results meet in shared memory: all at once for up to 8 heads, in two rounds for 16
+            constexpr int kRounds = kBoth ? 2 : 1, kPerRound = C::kWarps / kRounds;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
+                l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+            }
+            float acc[kShare], top_all[kShare], sum_all[kShare];
+#pragma unroll
+            for (int x = 0; x < kShare; ++x) acc[x] = 0.f, sum_all[x] = 0.f, top_all[x] = -CUDART_INF_F;
+#pragma unroll
+            for (int round = 0; round < kRounds; ++round) {
+                if (round) __syncthreads();
+                if (warp / kPerRound == round) {
+#pragma unroll
+                    for (int y = 0; y < (kBoth ? 2 : 1); ++y) {
+                        float *j = s_join + ((warp % kPerRound) * GC + gr + 8 * y) * C::kPitch;
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<float2 *>(j + c * 8 + gc * 2) = make_float2(o[c][2 * y], o[c][2 * y + 1]);
+                        if (gc == 0) j[D] = m[y], j[D + 1] = l[y];
+                    }
+                }
+                __syncthreads();
+#pragma unroll
+                for (int x = 0; x < kShare; ++x) {
+                    const int e = x * 256 + tid, g = e / D, c = e % D;
+                    if (g >= nh) continue;
+                    float top = top_all[x];
+#pragma unroll
+                    for (int k = 0; k < kPerRound; ++k) top = fmaxf(top, s_join[(k * GC + g) * C::kPitch + D]);
+                    const float base = top == -CUDART_INF_F ? 0.f : top, f0 = ex2_approx(top_all[x] - base);
+                    acc[x] *= f0;
+                    sum_all[x] *= f0;
+#pragma unroll
+                    for (int k = 0; k < kPerRound; ++k) {
+                        const float *j = s_join + (k * GC + g) * C::kPitch;
+                        const float f = ex2_approx(j[D] - base);
+                        sum_all[x] += f * j[D + 1];
+                        acc[x] += f * j[c];
+                    }
+                    top_all[x] = top;
+                }
+            }
+            float *part = a.part + ((int64_t)blockIdx.x * 2 + (starts_inside || i + 1 != last ? 0 : 1)) * GC * (D + 2);
+#pragma unroll
+            for (int x = 0; x < kShare; ++x) {
+                const int e = x * 256 + tid, g = e / D, c = e % D;
+                if (g >= nh) continue;
+                const float sum = sum_all[x];
+                if (whole) {
+                    const int64_t h = (int64_t)cur.b * a.Hq + h0 + g;
+                    static_cast<__nv_bfloat16 *>(a.out)[h * D + c] =
+                        __float2bfloat16_rn(sum > 0.f || sum != sum ? acc[x] / sum : 0.f);
+                    if (c == 0 && a.lse)
+                        a.lse[h] = sum == 0.f ? -CUDART_INF_F : top_all[x] * 0.69314718055994531f + logf(sum);
+                } else {
+                    part[g * (D + 2) + 2 + c] = acc[x];
+                    if (c == 0) {
+                        part[g * (D + 2)] = top_all[x];
+                        part[g * (D + 2) + 1] = sum;
+                    }
+                }
+            }
+            __syncthreads();   // the buffer is read before the next pair's results
+            starts_inside = false;
+            fresh = true;
+        }
+    }
+    cp_async_wait<0>();
+}
+
+// Query heads that a block takes together.  fp32: the whole group up to 8 (their sums are registers of
+// every lane); bf16: 8 or 16, half or all rows of a fragment.  A larger group reads its cache again.
+inline int decode_group_chunk(int group, bool bf16) {
+    if (bf16) return group <= 8 ? 8 : 16;
+    return group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8;
+}
+
+inline size_t decode_workspace_bytes(int group, int d, bool bf16) {
+    return (size_t)kMaxDecodeBlocks * 2 * decode_group_chunk(group, bf16) * (d + 2) * 4;
+}
+
+template <typename T, int D, int GC, typename C> cudaError_t launch_decode_g(void (*kern)(DecodeArgs), int threads,
+                                                                             DecodeArgs a, int sms, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    a.vheads = a.Hkv * ((a.Hq / a.Hkv + GC - 1) / GC);
+    a.blocks = decode_blocks(a, C::kTile, sms);
+    kern<<<a.blocks, threads, C::kSmem, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_behind(attn_decode_join_kernel<T, D, GC, C::kTile>, (unsigned)((int64_t)a.n * a.vheads), 128, 0, st, a);
+}
+
+template <int D> cudaError_t launch_attn_decode_bf16(const DecodeArgs &a, int sms, cudaStream_t st) {
+    using T = __nv_bfloat16;
+    if (decode_group_chunk(a.Hq / a.Hkv, true) == 8)
+        return launch_decode_g<T, D, 8, DecodeMmaCfg<D, 8>>(attn_decode_mma_kernel<D, 8>, 256, a, sms, st);
+    return launch_decode_g<T, D, 16, DecodeMmaCfg<D, 16>>(attn_decode_mma_kernel<D, 16>, 256, a, sms, st);
+}
+
+template <int D> cudaError_t launch_attn_decode_f32(const DecodeArgs &a, int sms, cudaStream_t st) {
+    switch (decode_group_chunk(a.Hq / a.Hkv, false)) {
+        case 1: return launch_decode_g<float, D, 1, DecodeCfg<float, D, 1>>(attn_decode_kernel<float, D, 1>, 128, a, sms, st);
+        case 2: return launch_decode_g<float, D, 2, DecodeCfg<float, D, 2>>(attn_decode_kernel<float, D, 2>, 128, a, sms, st);
+        case 4: return launch_decode_g<float, D, 4, DecodeCfg<float, D, 4>>(attn_decode_kernel<float, D, 4>, 128, a, sms, st);
+        default: return launch_decode_g<float, D, 8, DecodeCfg<float, D, 8>>(attn_decode_kernel<float, D, 8>, 128, a, sms, st);
+    }
+}
+
+}  // namespace attn
+}  // namespace kda
