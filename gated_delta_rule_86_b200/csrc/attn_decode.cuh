@@ -34,6 +34,7 @@ struct DecodeArgs {
     float *lse;         // [n][Hq] or null
     float *part;        // workspace: 2 slots per block of [GC][D + 2]
     int blocks;         // blocks of the main kernel
+    int per_pair;       // one block per (sequence, head group), no shares and no join
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
@@ -109,6 +110,16 @@ template <int TILE> struct Walk {
     int64_t first, last;   // the share
     // Works the share out from the lengths; false if it is empty.  Every thread of the block.
     __device__ __forceinline__ bool start(const DecodeArgs &a, int64_t *scratch) {
+        if (a.per_pair) {
+            b = blockIdx.x / a.vheads;
+            vh = blockIdx.x % a.vheads;
+            tile = 0;
+            len = decode_len(a, b);
+            tiles = (len + TILE - 1) / TILE;
+            first = 0;
+            last = tiles;
+            return tiles > 0;
+        }
         int64_t mine = 0;
         for (int n = threadIdx.x; n < a.n; n += blockDim.x) mine += decode_tiles<TILE>(a, n);
         const int64_t all = block_sum(mine, scratch) * a.vheads;
@@ -149,6 +160,20 @@ template <typename T, int D, int GC> struct DecodeCfg {
     static constexpr int kJoin = kDecodeWarps * GC * (D + 2) * 4;
     static constexpr int kSmem = kRing + kQ + kP + kJoin + 160;
 };
+
+// What a block does for a pair without tokens where no join follows: zeros, lse -inf.
+template <typename T, int D, int GC> __device__ __forceinline__ void write_empty(const DecodeArgs &a, int b, int vh) {
+    const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv, hkv = vh / chunks, h0 = hkv * group + (vh % chunks) * GC;
+    const int nh = min(GC, hkv * group + group - h0);
+    T *out = static_cast<T *>(a.out) + ((int64_t)b * a.Hq + h0) * D;
+    for (int e = threadIdx.x; e < nh * D; e += blockDim.x) out[e] = from_f32<T>(0.f);
+    if (a.lse && threadIdx.x < nh) a.lse[(int64_t)b * a.Hq + h0 + threadIdx.x] = -CUDART_INF_F;
+}
+
+// A sequence longer than its row of the table is cut there, and reported.
+__device__ __forceinline__ void check_len(const DecodeArgs &a, int b) {
+    if (__ldg(a.lens + b) > decode_len(a, b)) record_device_error(kDevErrBadPage);
+}
 
 // Copies a warp's 16 tokens of the tile at `w` into its stage; returns a mask of the valid ones.
 template <typename T, int D, int TILE>
@@ -217,7 +242,12 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
 
     asm volatile("griddepcontrol.launch_dependents;");   // the join may take its place; it waits for this grid's end
     Walk<C::kTile> w;
-    if (!w.start(a, scratch)) return;
+    const bool work = w.start(a, scratch);
+    if (a.per_pair && tid == 0) check_len(a, w.b);
+    if (!work) {
+        if (a.per_pair) write_empty<T, D, GC>(a, w.b, w.vh);
+        return;
+    }
     const int64_t first = w.first, last = w.last;
     Walk<C::kTile> ahead = w;
 
@@ -405,14 +435,13 @@ __global__ void __launch_bounds__(128) attn_decode_join_kernel(const DecodeArgs 
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the main kernel's parts, from here on
     const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv, hkv = vh / chunks, h0 = hkv * group + (vh % chunks) * GC;
     const int nh = min(GC, hkv * group + group - h0);
-    const int len = decode_len(a, b), tiles = decode_tiles<TILE>(a, b);
-    if (tid == 0 && vh == 0 && __ldg(a.lens + b) > len) record_device_error(kDevErrBadPage);
-    T *out = static_cast<T *>(a.out) + ((int64_t)b * a.Hq + h0) * D;
+    const int tiles = decode_tiles<TILE>(a, b);
+    if (tid == 0 && vh == 0) check_len(a, b);
     if (tiles == 0) {
-        for (int e = tid; e < nh * D; e += blockDim.x) out[e] = from_f32<T>(0.f);
-        if (a.lse && tid < nh) a.lse[(int64_t)b * a.Hq + h0 + tid] = -CUDART_INF_F;
+        write_empty<T, D, GC>(a, b, vh);
         return;
     }
+    T *out = static_cast<T *>(a.out) + ((int64_t)b * a.Hq + h0) * D;
     const int64_t s0 = before + (int64_t)vh * tiles, s1 = s0 + tiles;
     // blocks whose share [all c / blocks, all (c + 1) / blocks) meets [s0, s1)
     int64_t c0 = s0 * a.blocks / all, c1 = (s1 - 1) * a.blocks / all;
@@ -423,18 +452,24 @@ __global__ void __launch_bounds__(128) attn_decode_join_kernel(const DecodeArgs 
     if (c0 == c1) return;   // one block had it all and wrote the output
     for (int e = tid; e < nh * D; e += blockDim.x) {
         const int g = e / D, c = e % D;
+        // a block's part: slot 0 if the pair began before its share, slot 1 otherwise; none if its share is empty
+        auto part_of = [&](int64_t k) {
+            const int64_t from = all * k / a.blocks, to = all * (k + 1) / a.blocks;
+            return from < to ? a.part + ((k * 2 + (s0 < from ? 0 : 1)) * GC + g) * (D + 2) : nullptr;
+        };
         float top = -CUDART_INF_F, sum = 0.f, acc = 0.f;
+#pragma unroll 4
         for (int64_t k = c0; k <= c1; ++k) {
-            // the pair is the block's first if it began at or before the share's begin
-            const int64_t from = all * k / a.blocks;
-            if (from >= all * (k + 1) / a.blocks) continue;   // an empty share
-            const int slot = s0 < from ? 0 : 1;
-            const float *p = a.part + ((k * 2 + slot) * GC + g) * (D + 2);
-            const float mk = p[0], mn = fmaxf(top, mk), base = mn == -CUDART_INF_F ? 0.f : mn;
-            const float f = exp2f(top - base), fk = exp2f(mk - base);
-            sum = sum * f + p[1] * fk;
-            acc = acc * f + p[2 + c] * fk;
-            top = mn;
+            const float *p = part_of(k);
+            top = fmaxf(top, p ? p[0] : -CUDART_INF_F);
+        }
+        const float base = top == -CUDART_INF_F ? 0.f : top;
+#pragma unroll 4
+        for (int64_t k = c0; k <= c1; ++k) {
+            const float *p = part_of(k);
+            const float f = p ? exp2f(p[0] - base) : 0.f;
+            sum += p ? p[1] * f : 0.f;
+            acc += p ? p[2 + c] * f : 0.f;
         }
         out[g * D + c] = from_f32<T>(sum > 0.f || sum != sum ? acc / sum : 0.f);
         if (c == 0 && a.lse)

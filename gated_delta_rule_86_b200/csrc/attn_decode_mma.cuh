@@ -35,6 +35,33 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The page of a warp's first token of a tile, -1 where it has none; its lookup runs a tile ahead of its use.
+template <int TILE> __device__ __forceinline__ int first_page(const DecodeArgs &a, const Walk<TILE> &w, int warp) {
+    const int tok = w.tile * TILE + warp * kWarpTokens;
+    return tok < w.len ? __ldg(a.cache.table + w.b * a.cache.row + (tok >> a.cache.page_log2)) : -1;
+}
+
+// load_tokens where the 16 tokens all exist and lie on one good page (`page`): 16 rows side by side in
+// memory, so that a lane's addresses are one base and constants.
+template <int D, int TILE>
+__device__ __forceinline__ void load_whole(const DecodeArgs &a, const Walk<TILE> &w, int warp, int lane, int hkv,
+                                           uint32_t stage, int page) {
+    constexpr int CH = D * 2 / 16, ROWS = 32 / CH, N = kWarpTokens / ROWS;   // rows of one instruction, instructions
+    const int t0 = w.tile * TILE + warp * kWarpTokens;
+    const int64_t slot = ((int64_t)hkv << a.cache.page_log2) + (t0 & ((1 << a.cache.page_log2) - 1));
+    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.cache.k) + page * a.cache.k_stride + slot * D + lane * 8;
+    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.cache.v) + page * a.cache.v_stride + slot * D + lane * 8;
+    // chunk c of row r lies at chunk (c ^ r) & 7 of its half row; r = i ROWS + r_lane, the two apart in their bits
+    const int rl = lane / CH, c = lane % CH;
+    const uint32_t at = rl * (CH * 16) + (((c & ~7) | ((c ^ rl) & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t dst = stage + i * (ROWS * CH * 16) + (at ^ ((i * ROWS & 7) << 4));
+        cp_async16(dst, k + i * ROWS * D, true);
+        cp_async16(dst + kWarpTokens * CH * 16, v + i * ROWS * D, true);
+    }
+}
+
 template <int D, int GC> struct DecodeMmaCfg {
     static constexpr int kWarps = 8;
     static constexpr int kTile = kWarps * kWarpTokens;
@@ -64,9 +91,27 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
 
     asm volatile("griddepcontrol.launch_dependents;");   // the join may take its place; it waits for this grid's end
     Walk<C::kTile> w;
-    if (!w.start(a, scratch)) return;
+    const bool work = w.start(a, scratch);
+    if (a.per_pair && tid == 0) check_len(a, w.b);
+    if (!work) {
+        if (a.per_pair) write_empty<__nv_bfloat16, D, GC>(a, w.b, w.vh);
+        return;
+    }
     const int64_t last = w.last;
     Walk<C::kTile> ahead = w;
+    int page = first_page(a, ahead, warp);
+    // loads the tile at `ahead` into a stage and moves on
+    auto load = [&](uint32_t stage, int hkv) {
+        uint32_t got = 0xffffu;
+        const int tok = ahead.tile * C::kTile + warp * kWarpTokens;
+        if (a.cache.page_log2 >= 4 && tok + kWarpTokens <= ahead.len && page >= 0 && page < a.cache.num_pages)
+            load_whole<D, C::kTile>(a, ahead, warp, lane, hkv, stage, page);
+        else
+            got = tok < ahead.len ? load_tokens<__nv_bfloat16, D, C::kTile>(a, ahead, warp, lane, hkv, stage) : 0;
+        ahead.next(a);
+        page = first_page(a, ahead, warp);
+        return got;
+    };
     const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv;
     uint32_t held[C::kStages];   // which of a stage's tokens there are
 #pragma unroll
@@ -75,8 +120,7 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
 #pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s) {
         if (issued < last) {
-            held[s] = load_tokens<__nv_bfloat16, D, C::kTile>(a, ahead, warp, lane, ahead.vh / chunks, ring + s * C::kStageBytes);
-            ahead.next(a);
+            held[s] = load(ring + s * C::kStageBytes, ahead.vh / chunks);
             ++issued;
         }
         cp_async_commit();
@@ -85,6 +129,8 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
     // this lane's addresses inside a stage: ldmatrix rows
     const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;   // K: tokens 0-7 | 8-15, chunk 0 | 1
     const int vrow = lane & 15, vch = lane >> 4;                               // V: tokens 0-15, chunk 0 | 1
+    const uint32_t kat = krow * (CH * 16) + (((kch ^ krow) & 7) << 4);
+    const uint32_t vat = kWarpTokens * C::kRowBytes + vrow * (CH * 16) + (((vch ^ vrow) & 7) << 4);
     uint32_t qf[D / 16][4];
     float o[D / 8][4];
     float m[2], l[2];
@@ -117,9 +163,7 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
             uint32_t got = 0;
             const int into = st == 0 ? C::kStages - 1 : st - 1;
             if (issued < last) {
-                got = load_tokens<__nv_bfloat16, D, C::kTile>(a, ahead, warp, lane, ahead.vh / chunks,
-                                                              ring + into * C::kStageBytes);
-                ahead.next(a);
+                got = load(ring + into * C::kStageBytes, ahead.vh / chunks);
                 ++issued;
             }
             cp_async_commit();
@@ -134,13 +178,12 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
         for (int s = 0; s < C::kStages; ++s)
             if (s == st) ok = held[s];
         if (ok) {   // a warp's share of the tile may be empty
-            const uint32_t ks = ring + st * C::kStageBytes, vs = ks + kWarpTokens * C::kRowBytes;
+            const uint32_t ks = ring + st * C::kStageBytes;
             float s0[4] = {}, s1[4] = {};   // tokens 0-7, 8-15
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 uint32_t b[4];
-                const int c = kk * 2 + kch;
-                ldsm4(b, ks + krow * (CH * 16) + (((c & ~7) | ((c ^ krow) & 7)) << 4));
+                ldsm4(b, ks + (kat ^ ((2 * kk & 7) << 4)) + (kk >> 2) * 128);
                 mma_bf16(s0, qf[kk], b[0], b[1]);
                 mma_bf16(s1, qf[kk], b[2], b[3]);
             }
@@ -151,8 +194,12 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
             for (int y = 0; y < (kBoth ? 2 : 1); ++y) {
                 float x[4] = {s0[2 * y], s0[2 * y + 1], s1[2 * y], s1[2 * y + 1]};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[e] = (ok >> (2 * gc + (e & 1) + (e >> 1) * 8)) & 1 ? x[e] * sc : -CUDART_INF_F;
+                for (int e = 0; e < 4; ++e) x[e] *= sc;
+                if (ok != 0xffffu) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!((ok >> (2 * gc + (e & 1) + (e >> 1) * 8)) & 1)) x[e] = -CUDART_INF_F;
+                }
                 float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -185,8 +232,7 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
 #pragma unroll
             for (int c2 = 0; c2 < D / 16; ++c2) {
                 uint32_t b[4];
-                const int c = c2 * 2 + vch;
-                ldsm4_t(b, vs + vrow * (CH * 16) + (((c & ~7) | ((c ^ vrow) & 7)) << 4));
+                ldsm4_t(b, ks + (vat ^ ((2 * c2 & 7) << 4)) + (c2 >> 2) * 128);
                 mma_bf16(o[2 * c2], p, b[0], b[1]);
                 mma_bf16(o[2 * c2 + 1], p, b[2], b[3]);
             }
@@ -277,6 +323,8 @@ inline int decode_group_chunk(int group, bool bf16) {
     return group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8;
 }
 
+constexpr int kPairTokens = 1024;
+
 inline size_t decode_workspace_bytes(int group, int d, bool bf16) {
     return (size_t)kMaxDecodeBlocks * 2 * decode_group_chunk(group, bf16) * (d + 2) * 4;
 }
@@ -286,9 +334,12 @@ template <typename T, int D, int GC, typename C> cudaError_t launch_decode_g(voi
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     a.vheads = a.Hkv * ((a.Hq / a.Hkv + GC - 1) / GC);
-    a.blocks = decode_blocks(a, C::kTile, sms);
+    // Short contexts of few pairs: a block takes a whole pair, which saves the join and its launch
+    const int64_t pairs = (int64_t)a.n * a.vheads, tokens = (int64_t)a.cache.width << a.cache.page_log2;
+    a.per_pair = pairs <= sms && tokens <= kPairTokens;
+    a.blocks = a.per_pair ? (int)pairs : decode_blocks(a, C::kTile, sms);
     kern<<<a.blocks, threads, C::kSmem, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess || a.per_pair) return e;
     return launch_behind(attn_decode_join_kernel<T, D, GC, C::kTile>, (unsigned)((int64_t)a.n * a.vheads), 128, 0, st, a);
 }
 
