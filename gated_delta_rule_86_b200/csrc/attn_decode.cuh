@@ -50,12 +50,20 @@ __device__ __forceinline__ int decode_len(const DecodeArgs &a, int b) {
     const int64_t most = (int64_t)a.cache.width << a.cache.page_log2;
     return (int)min((int64_t)max(__ldg(a.lens + b), 0), most);
 }
+// What a pair costs beside its tiles (its queries, the join of the warps), in tiles: it counts in the shares,
+// or blocks with many short pairs would end long after the others.
+constexpr int kPairCost = 2;
 template <int TILE> __device__ __forceinline__ int decode_tiles(const DecodeArgs &a, int b) {
     return (decode_len(a, b) + TILE - 1) / TILE;
 }
 
-// Where the line of tiles stands before sequence b_stop, and (out) its whole length, in tiles of one
-// head group.  Every thread of the block calls it and gets the same answer.
+// Length of a pair on the line.
+template <int TILE> __device__ __forceinline__ int decode_units(const DecodeArgs &a, int b) {
+    const int t = decode_tiles<TILE>(a, b);
+    return t > 0 ? t + kPairCost : 0;
+}
+
+// Sum over the block; every thread gets it.
 __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *scratch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
@@ -68,7 +76,7 @@ __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *scratch) {
     return x;
 }
 
-// First sequence whose tiles reach beyond `want` (in tiles of one head group), and the tiles before it.
+// The sequence that holds place `want` of the line (counted for one head group), and its begin.
 template <int TILE>
 __device__ __forceinline__ void find_sequence(const DecodeArgs &a, int64_t want, int64_t *scratch, int &seq,
                                               int64_t &before) {
@@ -76,7 +84,7 @@ __device__ __forceinline__ void find_sequence(const DecodeArgs &a, int64_t want,
     int64_t at = 0;
     for (int base = 0; base < a.n; base += blockDim.x) {
         const int b = base + threadIdx.x;
-        const int64_t mine = b < a.n ? decode_tiles<TILE>(a, b) : 0;
+        const int64_t mine = b < a.n ? decode_units<TILE>(a, b) : 0;
         int64_t upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -104,10 +112,22 @@ __device__ __forceinline__ void find_sequence(const DecodeArgs &a, int64_t want,
     __syncthreads();
 }
 
+// The line of `all` tiles in `blocks` shares that differ by one tile at most.
+struct Shares {
+    int64_t per, rem;   // the first `rem` shares have per + 1 tiles
+    __device__ __forceinline__ Shares(int64_t all, int blocks) : per(all / blocks), rem(all % blocks) {}
+    __device__ __forceinline__ int64_t begin(int64_t c) const { return c * per + min(c, rem); }
+    // the share that holds tile t
+    __device__ __forceinline__ int64_t of(int64_t t) const {
+        const int64_t wide = rem * (per + 1);
+        return t < wide ? t / (per + 1) : rem + (t - wide) / per;
+    }
+};
+
 // Walks the tiles of a block's share of the line.
 template <int TILE> struct Walk {
     int b, vh, tile, tiles, len;
-    int64_t first, last;   // the share
+    int64_t at, last;   // place on the line, the share's end
     // Works the share out from the lengths; false if it is empty.  Every thread of the block.
     __device__ __forceinline__ bool start(const DecodeArgs &a, int64_t *scratch) {
         if (a.per_pair) {
@@ -116,36 +136,45 @@ template <int TILE> struct Walk {
             tile = 0;
             len = decode_len(a, b);
             tiles = (len + TILE - 1) / TILE;
-            first = 0;
+            at = 0;
             last = tiles;
             return tiles > 0;
         }
         int64_t mine = 0;
-        for (int n = threadIdx.x; n < a.n; n += blockDim.x) mine += decode_tiles<TILE>(a, n);
+        for (int n = threadIdx.x; n < a.n; n += blockDim.x) mine += decode_units<TILE>(a, n);
         const int64_t all = block_sum(mine, scratch) * a.vheads;
-        first = all * blockIdx.x / a.blocks;
-        last = all * (blockIdx.x + 1) / a.blocks;
-        if (first >= last) return false;
+        const Shares sh(all, a.blocks);
+        at = sh.begin(blockIdx.x);
+        last = sh.begin(blockIdx.x + 1);
+        if (at >= last) return false;
         int64_t before;
-        find_sequence<TILE>(a, first / a.vheads, scratch, b, before);
+        find_sequence<TILE>(a, at / a.vheads, scratch, b, before);
         len = decode_len(a, b);
         tiles = (len + TILE - 1) / TILE;
-        const int64_t in_seq = first - before * a.vheads;
-        vh = (int)(in_seq / tiles);
-        tile = (int)(in_seq % tiles);
-        return true;
+        const int64_t in_seq = at - before * a.vheads;
+        vh = (int)(in_seq / (tiles + kPairCost));
+        tile = (int)(in_seq % (tiles + kPairCost));
+        if (tile >= tiles) {   // the share begins behind a pair's last tile
+            at -= tile - (tiles - 1);
+            tile = tiles - 1;
+            next(a);
+        }
+        return at < last;
     }
     __device__ __forceinline__ void next(const DecodeArgs &a) {
+        ++at;
         if (++tile < tiles) return;
+        at += kPairCost;
         tile = 0;
         if (++vh < a.vheads) return;
         vh = 0;
-        do {   // the caller stops at its share's end, so there is a next sequence when this is used
+        do {   // behind the last sequence: any length, the caller stops there
             ++b;
             len = b < a.n ? decode_len(a, b) : TILE;
         } while (len == 0);
         tiles = (len + TILE - 1) / TILE;
     }
+    __device__ __forceinline__ bool more() const { return at < last; }
 };
 
 template <typename T, int D, int GC> struct DecodeCfg {
@@ -248,20 +277,17 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
         if (a.per_pair) write_empty<T, D, GC>(a, w.b, w.vh);
         return;
     }
-    const int64_t first = w.first, last = w.last;
     Walk<C::kTile> ahead = w;
 
     const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv;
     uint32_t valid[C::kStages];
-    int64_t issued = first;
 #pragma unroll
     for (int s = 0; s < C::kStages; ++s) valid[s] = 0;
 #pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s) {
-        if (issued < last) {
+        if (ahead.more()) {
             valid[s] = load_tokens<T, D, C::kTile>(a, ahead, warp, lane, ahead.vh / chunks, ring + s * C::kStageBytes);
             ahead.next(a);
-            ++issued;
         }
         cp_async_commit();
     }
@@ -272,7 +298,7 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
     bool starts_inside = w.tile != 0;   // the first pair began in an earlier block
     bool fresh = true;
     int st = 0;
-    for (int64_t i = first; i < last; ++i) {
+    while (w.more()) {
         const int hkv = w.vh / chunks, h0 = hkv * group + (w.vh % chunks) * GC;
         const int nh = min(GC, hkv * group + group - h0);
         if (fresh) {   // a new pair: its queries, scaled so that exp is 2^x
@@ -297,10 +323,9 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
         {
             const int into = (st + C::kStages - 1) % C::kStages;
             uint32_t got = 0;
-            if (issued < last) {
+            if (ahead.more()) {
                 got = load_tokens<T, D, C::kTile>(a, ahead, warp, lane, ahead.vh / chunks, ring + into * C::kStageBytes);
                 ahead.next(a);
-                ++issued;
             }
             cp_async_commit();
 #pragma unroll
@@ -362,8 +387,9 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
 
         st = (st + 1) % C::kStages;
         const Walk<C::kTile> cur = w;
-        if (i + 1 < last) w.next(a);
-        if (i + 1 == last || w.b != cur.b || w.vh != cur.vh) {
+        w.next(a);
+        const bool end = !w.more();
+        if (end || w.b != cur.b || w.vh != cur.vh) {
             // the end of this block's part of a pair: join the warps
             const bool ends_inside = cur.tile + 1 < cur.tiles;
             const bool whole = !starts_inside && !ends_inside;
@@ -382,7 +408,7 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
             }
             __syncthreads();
             // the first pair of a share leaves its part in slot 0, the last in slot 1
-            float *part = a.part + ((int64_t)blockIdx.x * 2 + (starts_inside || i + 1 != last ? 0 : 1)) * GC * (D + 2);
+            float *part = a.part + ((int64_t)blockIdx.x * 2 + (starts_inside || !end ? 0 : 1)) * GC * (D + 2);
             for (int e = tid; e < nh * D; e += blockDim.x) {
                 const int g = e / D, c = e % D;
                 float top = -CUDART_INF_F;
@@ -419,61 +445,64 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
 }
 
 // Joins the parts of every pair that more than one block worked on, and writes the rows of sequences
-// without a token (zeros, lse -inf).  One block per (sequence, head group); thread c owns channel c.
+// without a token (zeros, lse -inf).  One block per (sequence, head group), one warp per head; the parts
+// of a head are read several at a time, since each read waits for L2.
+constexpr int kJoinThreads = 256;
 template <typename T, int D, int GC, int TILE>
-__global__ void __launch_bounds__(128) attn_decode_join_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const DecodeArgs a) {
+    constexpr int CPL = D / 32;   // channels of a lane
     __shared__ int64_t scratch[20];
-    const int tid = threadIdx.x, b = blockIdx.x / a.vheads, vh = blockIdx.x % a.vheads;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x / a.vheads, vh = blockIdx.x % a.vheads;
     int64_t all = 0, before = 0;
     for (int n = tid; n < a.n; n += blockDim.x) {
-        const int t = decode_tiles<TILE>(a, n);
+        const int t = decode_units<TILE>(a, n);
         all += t;
         if (n < b) before += t;
     }
     all = block_sum(all, scratch) * a.vheads;
     before = block_sum(before, scratch) * a.vheads;
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the main kernel's parts, from here on
     const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv, hkv = vh / chunks, h0 = hkv * group + (vh % chunks) * GC;
     const int nh = min(GC, hkv * group + group - h0);
     const int tiles = decode_tiles<TILE>(a, b);
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the main kernel's parts, from here on
     if (tid == 0 && vh == 0) check_len(a, b);
     if (tiles == 0) {
         write_empty<T, D, GC>(a, b, vh);
         return;
     }
-    T *out = static_cast<T *>(a.out) + ((int64_t)b * a.Hq + h0) * D;
-    const int64_t s0 = before + (int64_t)vh * tiles, s1 = s0 + tiles;
-    // blocks whose share [all c / blocks, all (c + 1) / blocks) meets [s0, s1)
-    int64_t c0 = s0 * a.blocks / all, c1 = (s1 - 1) * a.blocks / all;
-    while (all * (c0 + 1) / a.blocks <= s0) ++c0;
-    while (c0 > 0 && all * c0 / a.blocks > s0) --c0;
-    while (all * (c1 + 1) / a.blocks <= s1 - 1) ++c1;
-    while (c1 > 0 && all * c1 / a.blocks > s1 - 1) --c1;
+    const Shares sh(all, a.blocks);
+    const int64_t s0 = before + (int64_t)vh * (tiles + kPairCost);
+    const int c0 = (int)sh.of(s0), c1 = (int)sh.of(s0 + tiles - 1);
     if (c0 == c1) return;   // one block had it all and wrote the output
-    for (int e = tid; e < nh * D; e += blockDim.x) {
-        const int g = e / D, c = e % D;
-        // a block's part: slot 0 if the pair began before its share, slot 1 otherwise; none if its share is empty
-        auto part_of = [&](int64_t k) {
-            const int64_t from = all * k / a.blocks, to = all * (k + 1) / a.blocks;
-            return from < to ? a.part + ((k * 2 + (s0 < from ? 0 : 1)) * GC + g) * (D + 2) : nullptr;
+    for (int g = warp; g < nh; g += kJoinThreads / 32) {
+        // the first block's part lies in its slot 0 if the pair began before its share; the others' in slot 0
+        auto part_of = [&](int k) {
+            return a.part + (((int64_t)k * 2 + (s0 < sh.begin(k) ? 0 : 1)) * GC + g) * (D + 2);
         };
-        float top = -CUDART_INF_F, sum = 0.f, acc = 0.f;
-#pragma unroll 4
-        for (int64_t k = c0; k <= c1; ++k) {
-            const float *p = part_of(k);
-            top = fmaxf(top, p ? p[0] : -CUDART_INF_F);
-        }
+        float top = -CUDART_INF_F, sum = 0.f, acc[CPL];
+        for (int k = c0 + lane; k <= c1; k += 32) top = fmaxf(top, part_of(k)[0]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float base = top == -CUDART_INF_F ? 0.f : top;
-#pragma unroll 4
-        for (int64_t k = c0; k <= c1; ++k) {
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
+#pragma unroll 8
+        for (int k = c0; k <= c1; ++k) {
             const float *p = part_of(k);
-            const float f = p ? exp2f(p[0] - base) : 0.f;
-            sum += p ? p[1] * f : 0.f;
-            acc += p ? p[2 + c] * f : 0.f;
+            const float f = exp2f(p[0] - base);
+            sum += p[1] * f;
+#pragma unroll
+            for (int c = 0; c < CPL; c += 2) {
+                const float2 x = *reinterpret_cast<const float2 *>(p + 2 + lane * CPL + c);
+                acc[c] += x.x * f;
+                acc[c + 1] += x.y * f;
+            }
         }
-        out[g * D + c] = from_f32<T>(sum > 0.f || sum != sum ? acc / sum : 0.f);
-        if (c == 0 && a.lse)
-            a.lse[(int64_t)b * a.Hq + h0 + g] = sum == 0.f ? -CUDART_INF_F : top * 0.69314718055994531f + logf(sum);
+        const int64_t h = (int64_t)b * a.Hq + h0 + g;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c)
+            static_cast<T *>(a.out)[h * D + lane * CPL + c] = from_f32<T>(sum > 0.f || sum != sum ? acc[c] / sum : 0.f);
+        if (lane == 0 && a.lse) a.lse[h] = sum == 0.f ? -CUDART_INF_F : top * 0.69314718055994531f + logf(sum);
     }
 }
 

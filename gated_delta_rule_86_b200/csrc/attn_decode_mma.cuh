@@ -97,7 +97,6 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
         if (a.per_pair) write_empty<__nv_bfloat16, D, GC>(a, w.b, w.vh);
         return;
     }
-    const int64_t last = w.last;
     Walk<C::kTile> ahead = w;
     int page = first_page(a, ahead, warp);
     // loads the tile at `ahead` into a stage and moves on
@@ -116,13 +115,9 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
     uint32_t held[C::kStages];   // which of a stage's tokens there are
 #pragma unroll
     for (int s = 0; s < C::kStages; ++s) held[s] = 0;
-    int64_t issued = w.first;
 #pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s) {
-        if (issued < last) {
-            held[s] = load(ring + s * C::kStageBytes, ahead.vh / chunks);
-            ++issued;
-        }
+        if (ahead.more()) held[s] = load(ring + s * C::kStageBytes, ahead.vh / chunks);
         cp_async_commit();
     }
 
@@ -137,20 +132,26 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
     const float sc = a.scale * kLog2e;
     bool starts_inside = w.tile != 0, fresh = true;
     int st = 0;
-    for (int64_t i = w.first; i < last; ++i) {
+    // the queries of the pair at w as the A operand
+    auto load_q = [&]() {
+        const int hkv = w.vh / chunks, h0 = hkv * group + (w.vh % chunks) * GC;
+        const int nh = min(GC, hkv * group + group - h0);
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                               w.b * a.q_stride + (int64_t)h0 * D);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const int c = kk * 8 + gc;
+            qf[kk][0] = gr < nh ? __ldg(q + gr * (D / 2) + c) : 0u;
+            qf[kk][2] = gr < nh ? __ldg(q + gr * (D / 2) + c + 4) : 0u;
+            qf[kk][1] = kBoth && gr + 8 < nh ? __ldg(q + (gr + 8) * (D / 2) + c) : 0u;
+            qf[kk][3] = kBoth && gr + 8 < nh ? __ldg(q + (gr + 8) * (D / 2) + c + 4) : 0u;
+        }
+    };
+    load_q();
+    while (w.more()) {
         const int hkv = w.vh / chunks, h0 = hkv * group + (w.vh % chunks) * GC;
         const int nh = min(GC, hkv * group + group - h0);
         if (fresh) {
-            const uint32_t *q = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                                   w.b * a.q_stride + (int64_t)h0 * D);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const int c = kk * 8 + gc;
-                qf[kk][0] = gr < nh ? __ldg(q + gr * (D / 2) + c) : 0u;
-                qf[kk][2] = gr < nh ? __ldg(q + gr * (D / 2) + c + 4) : 0u;
-                qf[kk][1] = kBoth && gr + 8 < nh ? __ldg(q + (gr + 8) * (D / 2) + c) : 0u;
-                qf[kk][3] = kBoth && gr + 8 < nh ? __ldg(q + (gr + 8) * (D / 2) + c + 4) : 0u;
-            }
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
 #pragma unroll
@@ -162,10 +163,7 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
         {
             uint32_t got = 0;
             const int into = st == 0 ? C::kStages - 1 : st - 1;
-            if (issued < last) {
-                got = load(ring + into * C::kStageBytes, ahead.vh / chunks);
-                ++issued;
-            }
+            if (ahead.more()) got = load(ring + into * C::kStageBytes, ahead.vh / chunks);
             cp_async_commit();
 #pragma unroll
             for (int s = 0; s < C::kStages; ++s)
@@ -241,8 +239,10 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
         st = st + 1 == C::kStages ? 0 : st + 1;
 
         const Walk<C::kTile> cur = w;
-        if (i + 1 < last) w.next(a);
-        if (i + 1 == last || w.b != cur.b || w.vh != cur.vh) {
+        w.next(a);
+        const bool end = !w.more();
+        if (end || w.b != cur.b || w.vh != cur.vh) {
+            if (!end) load_q();   // of the next pair: on their way during the join
             const bool whole = !starts_inside && cur.tile + 1 == cur.tiles;
             // the warps' results meet in shared memory: all at once for up to 8 heads, in two rounds for 16
             constexpr int kRounds = kBoth ? 2 : 1, kPerRound = C::kWarps / kRounds;
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
                     top_all[x] = top;
                 }
             }
-            float *part = a.part + ((int64_t)blockIdx.x * 2 + (starts_inside || i + 1 != last ? 0 : 1)) * GC * (D + 2);
+            float *part = a.part + ((int64_t)blockIdx.x * 2 + (starts_inside || !end ? 0 : 1)) * GC * (D + 2);
 #pragma unroll
             for (int x = 0; x < kShare; ++x) {
                 const int e = x * 256 + tid, g = e / D, c = e % D;
@@ -340,7 +340,7 @@ template <typename T, int D, int GC, typename C> cudaError_t launch_decode_g(voi
     a.blocks = a.per_pair ? (int)pairs : decode_blocks(a, C::kTile, sms);
     kern<<<a.blocks, threads, C::kSmem, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess || a.per_pair) return e;
-    return launch_behind(attn_decode_join_kernel<T, D, GC, C::kTile>, (unsigned)((int64_t)a.n * a.vheads), 128, 0, st, a);
+    return launch_behind(attn_decode_join_kernel<T, D, GC, C::kTile>, (unsigned)pairs, kJoinThreads, 0, st, a);
 }
 
 template <int D> cudaError_t launch_attn_decode_bf16(const DecodeArgs &a, int sms, cudaStream_t st) {
