@@ -78,7 +78,7 @@ def load() -> ctypes.CDLL:
         [ctypes.c_int, vp, vp, i64, i32, vp, vp, i64, i64, i32, i32, vp, vp, vp]
     lib.kda_attn_decode_step.argtypes = [vp, i64, vp, vp, i64, i64, i32, i32, vp, i64, i32, vp, i32, i32, i32, i32, f32,
                                          ctypes.c_int, vp, vp, vp, ctypes.c_size_t, vp]
-    lib.kda_attn_decode_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.c_int, size_p]
+    lib.kda_attn_decode_workspace_size.argtypes = [i32, i32, i32, i32, i64, ctypes.c_int, size_p]
     for name in EXPORTED[-6:]:
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib

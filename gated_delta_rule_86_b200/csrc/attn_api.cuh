@@ -171,14 +171,14 @@ kda_status kda_kv_append(const void *q, const void *k, const void *v, int64_t q_
     return status_of(d == 64 ? launch_append_d<__nv_bfloat16, 64>(a, st) : launch_append_d<__nv_bfloat16, 128>(a, st));
 }
 
-kda_status kda_attn_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype dtype,
-                                          size_t *bytes) {
+kda_status kda_attn_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int64_t max_tokens,
+                                          kda_dtype dtype, size_t *bytes) {
     using namespace kda::attn;
-    if (!bytes || B < 1) return KDA_ERR_INVALID_ARG;
+    if (!bytes || B < 1 || max_tokens < 1) return KDA_ERR_INVALID_ARG;
     *bytes = 0;
     const kda_status s = check_heads(Hq, Hkv, d, dtype);
     if (s != KDA_OK) return s;
-    *bytes = decode_workspace_bytes(Hq / Hkv, d, dtype == KDA_BF16);
+    *bytes = decode_workspace_bytes(B, Hq, Hkv, d, max_tokens, dtype == KDA_BF16, kda::device_sm_count());
     return KDA_OK;
 }
 
@@ -203,8 +203,10 @@ kda_status kda_attn_decode_step(const void *q, int64_t q_stride, const void *k_c
         KDA_OK)
         return s;
     if (heads != KDA_OK) return heads;
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < decode_workspace_bytes(Hq / Hkv, d, dtype == KDA_BF16))
-        return KDA_ERR_INVALID_ARG;
+    const int sms = kda::device_sm_count();
+    const size_t need = decode_workspace_bytes(B, Hq, Hkv, d, (int64_t)table_width << a.cache.page_log2,
+                                               dtype == KDA_BF16, sms);
+    if (!aligned(workspace, 16) || (need > 0 && !workspace) || workspace_bytes < need) return KDA_ERR_INVALID_ARG;
     if ((int64_t)B * Hq > 0x7fffffff) return KDA_ERR_UNSUPPORTED;
     if (((int64_t)table_width << a.cache.page_log2) > 0x7fffffff - 1024) return KDA_ERR_UNSUPPORTED;
     a.q = q;
@@ -217,7 +219,6 @@ kda_status kda_attn_decode_step(const void *q, int64_t q_stride, const void *k_c
     a.out = out;
     a.lse = lse;
     a.part = static_cast<float *>(workspace);
-    const int sms = kda::device_sm_count();
     if (sms < 1) return KDA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == KDA_F32)

@@ -323,10 +323,18 @@ inline int decode_group_chunk(int group, bool bf16) {
     return group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8;
 }
 
+// Short contexts of few pairs: a block takes a whole pair, which saves the join and its launch.  `tokens`:
+// what a row of the page table can hold.
 constexpr int kPairTokens = 1024;
+inline int64_t decode_pairs(int64_t n, int Hq, int Hkv, bool bf16) {
+    const int group = Hq / Hkv, gc = decode_group_chunk(group, bf16);
+    return n * Hkv * ((group + gc - 1) / gc);
+}
+inline bool decode_per_pair(int64_t pairs, int64_t tokens, int sms) { return pairs <= sms && tokens <= kPairTokens; }
 
-inline size_t decode_workspace_bytes(int group, int d, bool bf16) {
-    return (size_t)kMaxDecodeBlocks * 2 * decode_group_chunk(group, bf16) * (d + 2) * 4;
+inline size_t decode_workspace_bytes(int64_t n, int Hq, int Hkv, int d, int64_t tokens, bool bf16, int sms) {
+    if (decode_per_pair(decode_pairs(n, Hq, Hkv, bf16), tokens, sms)) return 0;
+    return (size_t)kMaxDecodeBlocks * 2 * decode_group_chunk(Hq / Hkv, bf16) * (d + 2) * 4;
 }
 
 template <typename T, int D, int GC, typename C> cudaError_t launch_decode_g(void (*kern)(DecodeArgs), int threads,
@@ -334,9 +342,8 @@ template <typename T, int D, int GC, typename C> cudaError_t launch_decode_g(voi
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     a.vheads = a.Hkv * ((a.Hq / a.Hkv + GC - 1) / GC);
-    // Short contexts of few pairs: a block takes a whole pair, which saves the join and its launch
     const int64_t pairs = (int64_t)a.n * a.vheads, tokens = (int64_t)a.cache.width << a.cache.page_log2;
-    a.per_pair = pairs <= sms && tokens <= kPairTokens;
+    a.per_pair = decode_per_pair(pairs, tokens, sms);
     a.blocks = a.per_pair ? (int)pairs : decode_blocks(a, C::kTile, sms);
     kern<<<a.blocks, threads, C::kSmem, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess || a.per_pair) return e;

@@ -420,7 +420,9 @@ kda_status kda_kv_append(const void *q, const void *k, const void *v, int64_t q_
  *               and tokens on a page outside the pool are left out; either makes
  *               the device error word KDA_ERR_BAD_PAGE.
  *   out       : [B, Hq, d];  lse : fp32 [B, Hq] or NULL.
- *   workspace : kda_attn_decode_workspace_size bytes, needing no initialisation.
+ *   workspace : kda_attn_decode_workspace_size bytes for this device and
+ *               max_tokens = table_width * page_size, needing no initialisation
+ *               (0 bytes, and NULL, for few sequences with short tables).
  * Slots past a sequence's end are never read.  The order of every sum is fixed
  * by the lengths: the same call gives the same bits.
  */
@@ -430,8 +432,8 @@ kda_status kda_attn_decode_step(const void *q, int64_t q_stride, const void *k_c
                                 int32_t table_width, const int32_t *seq_lens, int32_t B, int32_t Hq,
                                 int32_t Hkv, int32_t d, float scale, kda_dtype dtype, void *out,
                                 float *lse, void *workspace, size_t workspace_bytes, void *stream);
-kda_status kda_attn_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype dtype,
-                                          size_t *bytes);
+kda_status kda_attn_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int64_t max_tokens,
+                                          kda_dtype dtype, size_t *bytes);
 
 /* Human-readable name of a status (static string, never NULL). */
 const char *kda_status_string(kda_status s);

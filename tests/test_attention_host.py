@@ -38,7 +38,7 @@ def append(lib, q=F, k=F, v=F, qs=0, ks=0, vs=0, freq=F, rot=64, cu=None, n=0, B
                              vc, kp, vp, pages, size, qo, ko, None)
 
 
-def decode(lib, q=F, qs=0, kc=F, vc=F, kp=0, vp=0, pages=8, size=16, table=F, row=0, width=4, lens=F, B=1, Hq=4, Hkv=2,
+def decode(lib, q=F, qs=0, kc=F, vc=F, kp=0, vp=0, pages=8, size=16, table=F, row=0, width=400, lens=F, B=1, Hq=4, Hkv=2,
            d=64, scale=0.1, dt=B16, out=F, lse=None, ws=F, ws_bytes=1 << 30):
     return lib.kda_attn_decode_step(q, qs, kc, vc, kp, vp, pages, size, table, row, width, lens, B, Hq, Hkv, d, scale, dt,
                                     out, lse, ws, ws_bytes, None)
@@ -72,7 +72,7 @@ def test_gradient_workspace(lib):
 
 
 BAD_CACHE = [(dict(kc=None), E), (dict(vc=ODD), E), (dict(table=None), E), (dict(table=F + 2), E), (dict(pages=0), E),
-             (dict(size=0), E), (dict(width=0), E), (dict(row=3), E), (dict(kp=2 * 16 * 64 - 8), E),
+             (dict(size=0), E), (dict(width=0), E), (dict(width=4, row=3), E), (dict(kp=2 * 16 * 64 - 8), E),
              (dict(vp=2 * 16 * 64 + 4), E), (dict(size=24), U), (dict(size=1 << 17), U)]
 
 
@@ -95,9 +95,10 @@ def test_decode_refuses(lib, kw, want):
 
 def test_decode_workspace(lib):
     n = ctypes.c_size_t(0)
-    assert lib.kda_attn_decode_workspace_size(4, 8, 2, 128, B16, ctypes.byref(n)) == OK and n.value > 0
-    assert lib.kda_attn_decode_workspace_size(4, 8, 2, 96, B16, ctypes.byref(n)) == U and n.value == 0
-    assert lib.kda_attn_decode_workspace_size(4, 8, 3, 128, B16, ctypes.byref(n)) == E
+    assert lib.kda_attn_decode_workspace_size(4, 8, 2, 128, 1 << 20, B16, ctypes.byref(n)) == OK and n.value > 0
+    assert lib.kda_attn_decode_workspace_size(4, 8, 2, 96, 1 << 20, B16, ctypes.byref(n)) == U and n.value == 0
+    assert lib.kda_attn_decode_workspace_size(4, 8, 3, 128, 1 << 20, B16, ctypes.byref(n)) == E
+    assert lib.kda_attn_decode_workspace_size(4, 8, 2, 128, 0, B16, ctypes.byref(n)) == E
 
 
 def test_empty_calls_launch_nothing(lib):
