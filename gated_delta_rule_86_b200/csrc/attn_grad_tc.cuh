@@ -99,10 +99,6 @@ __device__ __forceinline__ void put_operand(uint32_t taddr, const float (&x)[32]
     tc::tmem_st16(taddr, u);
 }
 
-// Column of the A operand's k-step kk: each warpgroup writes its 64 columns' worth over the first half
-// of the columns that it read.
-__device__ __forceinline__ uint32_t operand_col(int kk) { return (kk >> 2) * 64 + (kk & 3) * 8; }
-
 __device__ __forceinline__ void arrive_operand(uint64_t *bar, int lane) {
     tc::tmem_st_wait();
     tc::tc_fence_before();

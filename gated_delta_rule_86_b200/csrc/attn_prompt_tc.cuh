@@ -7,11 +7,18 @@
 // (the same rows) where the group is even, two neighbouring row tiles of one head otherwise.  Both
 // products run on tcgen05 with fp32 accumulators in Tensor Memory: S (128 x 128) per tile, O (128 x d)
 // per tile.  Warp roles:
-//   warps 0-3, 4-7  softmax of tile 0 and 1: thread = row.  They read S, write P (bf16) over it as the
-//                   second product's A operand, and hold m and the sum in registers.
-//   warp 8          issues the products:  O_i += P_i V_j, then S_i = Q_i K_{j+1}, for i = 0, 1 in turn,
-//                   so one tile's softmax runs under the other tile's products.
-//   warp 9          TMA loads: Q once, then K_j, V_j through a ring of stages.
+//   warps 0-7, 8-15  softmax of tile 0 and 1: two threads per row, 64 columns each, which exchange their
+//                    maxima through shared memory.  They read S and write P (bf16) over what they read,
+//                    as the second product's A operand; m and the sum stay in registers.  (One thread per
+//                    row leaves one warp of a tile per scheduler, whose 128 powers in a row take longer
+//                    than both products: 905 TFLOP/s at 16384 tokens.)
+//   warp 16          issues the products:  O_i += P_i V_j, then S_i = Q_i K_{j+1}, for i = 0, 1 in turn, so
+//                    one tile's softmax runs under the other tile's products.
+//   warp 17          TMA loads: Q once, then K_j, V_j through a ring of stages.
+//   warp 18          waits for the loads on warp 16's behalf and joins its word to the softmax warps': a
+//                    wait behind products in flight returns only when they are done, so each one costs the
+//                    tensor pipe some 200 cycles.  It also zeroes the rows of the last V tile that lie
+//                    past the sequence's end.
 // m is allowed to lag: while a row's new maximum exceeds the m in use by less than 2^8 the weights are
 // only scaled differently (up to 2^8, exact in fp32 and no less precise in bf16), so O is rescaled
 // rarely, by the softmax warps themselves: S_i of a tile is issued after the previous O_i, and the
@@ -25,6 +32,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "attn_prompt.cuh"
 #include "kda_chunk_tc.cuh"
 #include "tc_utils.cuh"
@@ -33,6 +42,10 @@ namespace kda {
 namespace attn {
 
 constexpr int kTile = 128;   // queries of a tile, keys of a tile
+#ifndef EMU
+#define EMU 4
+#endif
+constexpr int kEmulate = EMU;  // one pair of weights in this many takes its power on the FMA units
 
 // ---- helpers shared with the gradient -----------------------------------------------------------
 
@@ -44,6 +57,10 @@ __device__ __forceinline__ uint64_t desc_k(uint32_t base, int kk) {
 __device__ __forceinline__ uint64_t desc_mn(uint32_t base, int kk) {
     return tc::make_sdesc(base + kk * 2048, kTile * 128, 1024, tc::kSwz128);
 }
+
+// An A operand in Tensor Memory that takes the place of fp32 columns: the threads that read 64 columns
+// write theirs as bf16 pairs over the first 32.  Column of k-step kk.
+__device__ __forceinline__ uint32_t operand_col(int kk) { return (kk >> 2) * 64 + (kk & 3) * 8; }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -67,9 +84,94 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+// The larger of three, NaN where one is: a score that is no number makes its row's maximum, and by it the whole row, NaN.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 2^x of two numbers on the FMA units, for x <= 127 and not NaN: x = n + f with |f| <= 1/2, 2^f by the
+// polynomial of degree 5 with the least largest relative error (7.5e-8, found by exchange; 2.1e-7 as
+// evaluated, no more than the SFU's), n added to the exponent.  Below -126 it stays at 2^-126.
+// The SFU gives 16 powers a clock and SM, so a tile of 128 x 128 weights takes as long as its two
+// products of depth 128; taking a part of the powers here shortens the longer of the two.
+__device__ __forceinline__ float2 ex2_fma(float2 x) {
+    x.x = fmaxf(x.x, -126.f);
+    x.y = fmaxf(x.y, -126.f);
+    constexpr float kRound = 12582912.f;   // 1.5 * 2^23: adding it rounds to a whole number
+    const float2 y = add2(x, make_float2(kRound, kRound));
+    const float2 n = add2(y, make_float2(-kRound, -kRound));
+    const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
+    float2 p = make_float2(1.3276472454890609e-3f, 1.3276472454890609e-3f);
+    p = fma2(p, f, make_float2(9.675540961325169e-3f, 9.675540961325169e-3f));
+    p = fma2(p, f, make_float2(5.550713092088699e-2f, 5.550713092088699e-2f));
+    p = fma2(p, f, make_float2(2.4022120237350464e-1f, 2.4022120237350464e-1f));
+    p = fma2(p, f, make_float2(6.931469440460205e-1f, 6.931469440460205e-1f));
+    p = fma2(p, f, make_float2(1.0000001192092896f, 1.0000001192092896f));
+    p.x = __int_as_float(__float_as_int(p.x) + (__float_as_int(y.x) << 23));
+    p.y = __int_as_float(__float_as_int(p.y) + (__float_as_int(y.y) << 23));
+    return p;
+}
+
+// Registers of a thread, moved between the warpgroups of a block after its launch: what one gives up
+// (kDown) another takes (kUp); 128 (2 kUp + kDown) may not exceed what the launch gave all three.
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // A whole warp's wait: one answer for all lanes, so that they leave loops together.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
     return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort));
+}
+
+// ---- products issued by a whole warp ----
+// The products' operands live in uniform registers.  In a branch of one lane the compiler moves every
+// descriptor there anew, some 60 cycles for each product; so the issuing warp stays together, one lane
+// elected once and for all issues, and the descriptors of a chain are the first one plus constants.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit_by(uint64_t *bar, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar)),
+        "r"(leader)
+        : "memory");
+}
+// d = x y^T over D columns of two K-major tiles (descriptors of their first k-step).
+template <int D> __device__ __forceinline__ void chain_ss(uint32_t d, uint64_t x, uint64_t y, uint32_t idesc, uint32_t leader) {
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t step = (kk >> 2) * (kTile * 128 / 16) + (kk & 3) * 2;
+        mma_ss(d, x + step, y + step, idesc, kk > 0, leader);
+    }
+}
+// d (+)= x y: x the operand in Tensor Memory over 128 columns, y an MN-major tile.
+__device__ __forceinline__ void chain_ts(uint32_t d, uint32_t x, uint64_t y, uint32_t idesc, bool accumulate, uint32_t leader) {
+#pragma unroll
+    for (int kk = 0; kk < kTile / 16; ++kk)
+        mma_ts(d, x + operand_col(kk), y + kk * 128, idesc, accumulate || kk > 0, leader);
 }
 
 // A head's tile of 128 tokens in 64-column blocks.
@@ -131,8 +233,12 @@ template <int D> struct FwdCfg {
     static constexpr int kQ = 0;                          // two query tiles
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kBars = kRing + kStages * kTileBytes;
-    static constexpr int kSmem = kBars + 512 + 1024;      // + alignment of the base
-    static constexpr int kThreads = 320;
+    static constexpr int kTop = kBars + 512;              // row maxima: [2 tiles][2 halves][128]
+    static constexpr int kSmem = kTop + 2 * 2 * kTile * 4;
+    static constexpr int kThreads = 640;
+    static constexpr int kUp = 104, kDown = 64;           // launched with 96 each: 128 (4 * 104 + 64) = 640 * 96
+    static_assert(4 * kUp + kDown <= 5 * 96, "registers");
+    static_assert(kSmem <= 232448, "shared memory");
 };
 
 struct FwdBars {
@@ -153,8 +259,7 @@ template <int D>
 __global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1)
 attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps, int pair_heads) {
     using C = FwdCfg<D>;
-    extern __shared__ uint8_t raw[];
-    uint8_t *smem = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     FwdBars &bars = *reinterpret_cast<FwdBars *>(smem + C::kBars);
     const uint32_t sbase = tc::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -185,7 +290,7 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars.q_full[i], 1);
             tc::mbar_init(&bars.s_full[i], 1);
-            tc::mbar_init(&bars.p_ready[i], 4);
+            tc::mbar_init(&bars.p_ready[i], 9);   // eight softmax warps and the loads'
             tc::mbar_init(&bars.o_full[i], 1);
         }
         for (int i = 0; i < C::kStages; ++i) {
@@ -195,7 +300,7 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
         tc::mbar_init(&bars.drain, 1);
         tc::fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == 16) {
         tc::tmem_alloc(&bars.tmem, 512);
         tc::tmem_relinquish();
     }
@@ -205,9 +310,11 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
     const uint32_t tmem = bars.tmem;
     volatile int *abort = &bars.abort;
     constexpr uint32_t kO = 256;
+    const int past = blocks * kTile - w.s.nk;   // rows of the last V tile behind the sequence's end
 
-    if (warp == 9) {
-        if (lane == 0 && blocks > 0) {
+    if (warp >= 16) {
+        regs_down<C::kDown>();
+        if (warp == 17 && lane == 0 && blocks > 0) {
             for (int i = 0; i < 2; ++i) {
                 if (w.blocks[i] == 0) continue;
                 tc::mbar_arrive_expect_tx(&bars.q_full[i], C::kTileBytes);
@@ -216,9 +323,8 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
             int st = 0, put = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int j = 0; j < 2 * blocks && ok; ++j) {   // K_0, V_0, K_1, ...
-                if (put >= C::kStages) ok = tc::mbar_wait(&bars.empty[st], ph ^ 1, abort);
-                if (!ok) break;
+            for (int j = 0; j < 2 * blocks; ++j) {   // K_0, V_0, K_1, ...
+                if (put >= C::kStages && !(ok = tc::mbar_wait(&bars.empty[st], ph ^ 1, abort))) break;
                 tc::mbar_arrive_expect_tx(&bars.full[st], C::kTileBytes);
                 tma_tile<D>(C::kRing + st * C::kTileBytes, smem, j & 1 ? &maps.v : &maps.k, w.hk,
                             w.s.k0 + (int64_t)(j >> 1) * kTile, &bars.full[st]);
@@ -235,96 +341,93 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                     tc::mbar_wait(&bars.full[k % C::kStages], (k / C::kStages) & 1, &quit);
                 }
             }
-        }
-    } else if (warp == 8) {
-        constexpr uint32_t idS = tc::make_idesc_bf16(kTile, kTile, false, false);
-        constexpr uint32_t idO = tc::make_idesc_bf16(kTile, D, false, true);
-        bool ok = true;
-        int st = 0;
-        uint32_t ph = 0;
-        auto scores = [&](int i, uint32_t ks) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                tc::mma_f16(tmem + i * kTile, desc_k(sbase + C::kQ + i * C::kTileBytes, kk), desc_k(ks, kk), idS, kk > 0);
-            tc::mma_commit(&bars.s_full[i]);
-        };
-        if (blocks > 0) {
-            ok = warp_wait(&bars.full[0], 0, abort);
+        } else if (warp == 18) {
+            bool ok = true;
+            for (int j = 0; j < blocks && ok; ++j) {
+                const int kv = 2 * j + 1, kn = kv + 1;
+                const bool more = j + 1 < blocks;
+                if (!(ok = warp_wait(&bars.full[kv % C::kStages], (kv / C::kStages) & 1, abort))) break;
+                if (past > 0 && !more) {
+                    zero_rows<D>(smem + C::kRing + (kv % C::kStages) * C::kTileBytes, kTile - past, lane);
+                    __syncwarp();
+                }
+                if (more && !(ok = warp_wait(&bars.full[kn % C::kStages], (kn / C::kStages) & 1, abort))) break;
+                if (lane == 0) {
+                    if (j < w.blocks[0]) tc::mbar_arrive(&bars.p_ready[0]);
+                    if (j < w.blocks[1]) tc::mbar_arrive(&bars.p_ready[1]);
+                }
+                // not ahead of the softmax: the next word belongs to the next turn
+                for (int i = 0; i < 2 && ok; ++i)
+                    if (j < w.blocks[i]) ok = warp_wait(&bars.p_ready[i], j & 1, abort);
+            }
+        } else if (warp == 16 && blocks > 0) {
+            constexpr uint32_t idS = tc::make_idesc_bf16(kTile, kTile, false, false);
+            constexpr uint32_t idO = tc::make_idesc_bf16(kTile, D, false, true);
+            const uint32_t leader = elect_lane();
+            // load number k (K_0, V_0, K_1, ...) lies in stage k mod kStages
+            auto loaded = [&](int k) { return warp_wait(&bars.full[k % C::kStages], (k / C::kStages) & 1, abort); };
+            auto scores = [&](int i, int st) {
+                chain_ss<D>(tmem + i * kTile, desc_k(sbase + C::kQ + i * C::kTileBytes, 0),
+                            desc_k(sbase + C::kRing + st * C::kTileBytes, 0), idS, leader);
+                commit_by(&bars.s_full[i], leader);
+            };
+            bool ok = loaded(0);
             for (int i = 0; i < 2 && ok; ++i) {
                 if (w.blocks[i] == 0) continue;
                 ok = warp_wait(&bars.q_full[i], 0, abort);
-                if (ok && lane == 0) scores(i, sbase + C::kRing);
+                if (ok) scores(i, 0);
             }
-            if (ok && lane == 0) tc::mma_commit(&bars.empty[0]);
-            st = 1;
-        }
-        for (int j = 0; j < blocks && ok; ++j) {
-            const int vst = st;
-            ok = warp_wait(&bars.full[vst], ph, abort);
-            if (!ok) break;
-            if (++st == C::kStages) st = 0, ph ^= 1;
-            const int left = w.s.nk - j * kTile;
-            if (left < kTile) {
-                zero_rows<D>(smem + C::kRing + vst * C::kTileBytes, left, lane);
-                __syncwarp();
-            }
-            const int kst = st;
-            bool have_k = false;
-            for (int i = 0; i < 2 && ok; ++i) {
-                if (j >= w.blocks[i]) continue;
-                ok = warp_wait(&bars.p_ready[i], j & 1, abort);
-                if (!ok) break;
-                tc::tc_fence_after();
-                if (lane == 0) {
+            if (ok) commit_by(&bars.empty[0], leader);
+            for (int j = 0; j < blocks && ok; ++j) {
+                const int kv = 2 * j + 1, kk1 = kv + 1;
+                const bool more = j + 1 < blocks;
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::mma_f16_ta(tmem + kO + i * D, tmem + i * kTile + kk * 8,
-                                       desc_mn(sbase + C::kRing + vst * C::kTileBytes, kk), idO, j > 0 || kk > 0);
+                for (int i = 0; i < 2; ++i) {
+                    if (j >= w.blocks[i]) continue;
+                    if (!(ok = warp_wait(&bars.p_ready[i], j & 1, abort))) break;
+                    tc::tc_fence_after();
+                    chain_ts(tmem + kO + i * D, tmem + i * kTile, desc_mn(sbase + C::kRing + (kv % C::kStages) * C::kTileBytes, 0),
+                             idO, j > 0, leader);
+                    if (j + 1 < w.blocks[i]) scores(i, kk1 % C::kStages);
+                    else commit_by(&bars.o_full[i], leader);
                 }
-                if (j + 1 < w.blocks[i]) {
-                    if (!have_k) {
-                        ok = warp_wait(&bars.full[kst], ph, abort);
-                        if (!ok) break;
-                        have_k = true;
-                    }
-                    if (lane == 0) scores(i, sbase + C::kRing + kst * C::kTileBytes);
-                } else if (lane == 0) {
-                    tc::mma_commit(&bars.o_full[i]);
-                }
+                if (!ok) break;
+                commit_by(&bars.empty[kv % C::kStages], leader);
+                if (more) commit_by(&bars.empty[kk1 % C::kStages], leader);
             }
-            if (!ok) break;
-            if (lane == 0) {
-                tc::mma_commit(&bars.empty[vst]);
-                if (have_k) tc::mma_commit(&bars.empty[kst]);
+            if (!ok) {   // no product in flight when the memory is given back
+                int quit = 0;
+                commit_by(&bars.drain, leader);
+                warp_wait(&bars.drain, 0, &quit);
             }
-            if (j + 1 < blocks && ++st == C::kStages) st = 0, ph ^= 1;
-        }
-        if (!ok && lane == 0) {   // no product in flight when the memory is given back
-            int quit = 0;
-            tc::mma_commit(&bars.drain);
-            tc::mbar_wait(&bars.drain, 0, &quit);
         }
         __syncwarp();
     } else {
-        const int i = warp >> 2, row = (warp & 3) * 32 + lane, r = w.r0[i] + row;
-        const uint32_t lanes = tc::tmem_lane_base(warp), tS = tmem + i * kTile + lanes, tO = tmem + kO + i * D + lanes;
-        const int seen = r < w.s.nq ? keys_seen(w.s, r, a.causal) : w.s.nk;
-        const int seen_all = keys_seen(w.s, min(w.r0[i] + (warp & 3) * 32, w.s.nq - 1), a.causal);   // by every row of the warp
+        regs_up<C::kUp>();
+        const int i = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane, r = w.r0[i] + row;
+        const uint32_t lanes = tc::tmem_lane_base(warp), tS = tmem + i * kTile + half * 64 + lanes,
+                       tO = tmem + kO + i * D + half * (D / 2) + lanes;
+        const int seen = (r < w.s.nq ? keys_seen(w.s, r, a.causal) : w.s.nk) - half * 64;
+        const int seen_all = keys_seen(w.s, min(w.r0[i] + quarter * 32, w.s.nq - 1), a.causal);   // by every row of the warp
         const float sc = a.scale * kLog2e;
+        const float lag = 8.f / sc;   // 2^8, in the scores' units
+        float *tops = reinterpret_cast<float *>(smem + C::kTop) + i * 2 * kTile + row;
+        const uint32_t pair = 1 + i * 4 + quarter;   // barrier of the two warps that share rows
         float m = -CUDART_INF_F, l = 0.f;
         bool ok = true;
         for (int j = 0; j < w.blocks[i]; ++j) {
             ok = warp_wait(&bars.s_full[i], j & 1, abort);
             if (!ok) break;
             tc::tc_fence_after();
-            float x[4][32];
+            float x[2][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + c * 32, x[c]);
+            for (int c = 0; c < 2; ++c) tc::tmem_ld32(tS + c * 32, x[c]);
             tc::tmem_ld_wait();
             const int c0 = j * kTile;
-            if (c0 + kTile > seen_all) {
+            const bool masked = c0 + kTile > seen_all;
+            if (masked) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (c0 + c * 32 + e >= seen) x[c][e] = -CUDART_INF_F;
@@ -332,66 +435,84 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
             float top[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                top[c] = x[c][0];
+                const float *y = &x[c >> 1][(c & 1) * 16];
+                top[c] = max3_nan(y[0], y[1], y[2]);
 #pragma unroll
-                for (int e = 1; e < 32; ++e) top[c] = fmaxf(top[c], x[c][e]);
+                for (int e = 3; e < 15; e += 2) top[c] = max3_nan(top[c], y[e], y[e + 1]);
+                top[c] = max3_nan(top[c], y[15], y[15]);
             }
-            const float mt = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
-            // the maximum in use follows the true one when it is 2^8 behind
-            const bool grow = (mt - m) * sc > 8.f;
+            float mt = max3_nan(max3_nan(top[0], top[1], top[2]), top[3], m);
+            // the row's other half.  It has read this one's by the next turn: the next scores wait for both's weights
+            tops[half * kTile] = mt;
+            tc::named_sync(pair, 64);
+            {
+                const float other = tops[(half ^ 1) * kTile];
+                mt = max3_nan(mt, other, other);
+            }
+            // the maximum in use follows the true one when it is 2^8 behind (or is NaN)
+            const bool grow = !(mt <= m + lag);
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? ex2_approx((m - mt) * sc) : 1.f;
                 if (grow) m = mt;
                 l *= f;
                 if (j > 0) {
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        tc::tmem_ld32(tO + c * 32, o);
+                    for (int c = 0; c < D / 32; ++c) {   // this half of the accumulator's columns
+                        float o[16];
+                        uint32_t u[16];
+                        tc::tmem_ld16(tO + c * 16, o);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; e += 16) {
-                            uint32_t u[16];
-#pragma unroll
-                            for (int y = 0; y < 16; ++y) u[y] = __float_as_uint(o[e + y] * f);
-                            tc::tmem_st16(tO + c * 32 + e, u);
-                        }
+                        for (int y = 0; y < 16; ++y) u[y] = __float_as_uint(o[y] * f);
+                        tc::tmem_st16(tO + c * 16, u);
                     }
                 }
             }
-            const float base = m == -CUDART_INF_F ? 0.f : -m * sc;
+            // an infinite maximum: no score at all (weights of zero), or one of +inf (NaN)
+            const float base = m == -CUDART_INF_F ? 0.f : m == CUDART_INF_F ? CUDART_NAN_F : -m * sc;
             const float2 sc2 = make_float2(sc, sc), base2 = make_float2(base, base);
             float2 sum = make_float2(0.f, 0.f);
+            auto weights = [&](auto plain) {   // plain: nothing hidden, so a part of the powers may go to the FMA units
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t u[16];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t u[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float2 y = fma2(make_float2(x[c][2 * e], x[c][2 * e + 1]), sc2, base2);
-                    y.x = ex2_approx(y.x);
-                    y.y = ex2_approx(y.y);
-                    sum = add2(sum, y);
-                    u[e] = pack_bf16(y.x, y.y);
+                    for (int e = 0; e < 16; ++e) {
+                        float2 y = fma2(make_float2(x[c][2 * e], x[c][2 * e + 1]), sc2, base2);
+                        if (plain.value && e % kEmulate == kEmulate - 1) {
+                            y = ex2_fma(y);
+                        } else {
+                            y.x = ex2_approx(y.x);
+                            y.y = ex2_approx(y.y);
+                        }
+                        sum = add2(sum, y);
+                        u[e] = pack_bf16(y.x, y.y);
+                    }
+                    tc::tmem_st16(tS + c * 16, u);
                 }
-                tc::tmem_st16(tS + c * 16, u);
-            }
-            l += sum.x + sum.y;
+            };
+            if (masked) weights(std::false_type{});
+            else weights(std::true_type{});
             tc::tmem_st_wait();
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars.p_ready[i]);
+            l += sum.x + sum.y;
         }
-        const int rows_left = w.s.nq - (w.r0[i] + (warp & 3) * 32);
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                             ((w.s.q0 + w.r0[i] + (warp & 3) * 32) * a.bt.Hq + w.head[i]) * (int64_t)D;
-        // Q_i's shared memory is free once O_i is complete
-        RowWriter<D> out{smem + C::kQ + i * C::kTileBytes + (warp & 3) * 32 * D * 2};
-        if (ok && w.blocks[i] > 0) {
-            ok = warp_wait(&bars.o_full[i], 0, abort);
+        if (ok && w.blocks[i] > 0) ok = warp_wait(&bars.o_full[i], 0, abort);
+        if (ok) {   // the sum of the row's two halves (both scaled by the same m)
+            tops[half * kTile] = l;
+            tc::named_sync(pair, 64);
+            l += tops[(half ^ 1) * kTile];
+        } else {   // a wait ran out: the other warp may stand at the barrier
+            asm volatile("bar.arrive %0, 64;" ::"r"(pair) : "memory");
         }
-        if (ok && rows_left > 0) {
+        const int rows_left = w.s.nq - (w.r0[i] + quarter * 32);
+        if (ok && rows_left > 0 && half == 0) {
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             tc::tc_fence_after();
+            // Q_i's shared memory is free once O_i is complete
+            RowWriter<D> out{smem + C::kQ + i * C::kTileBytes + quarter * 32 * D * 2};
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 float o[32];
@@ -405,15 +526,16 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                 }
                 out.put(lane, c, o, inv);
             }
-            out.flush(lane, dst, (int64_t)a.bt.Hq * D, rows_left);
+            out.flush(lane, static_cast<__nv_bfloat16 *>(a.out) +
+                                ((w.s.q0 + w.r0[i] + quarter * 32) * a.bt.Hq + w.head[i]) * (int64_t)D,
+                      (int64_t)a.bt.Hq * D, rows_left);
             if (a.lse && r < w.s.nq)
-                a.lse[stat_at(a.bt, w.s.q0 + r, w.head[i])] =
-                    l == 0.f ? -CUDART_INF_F : m * a.scale + logf(l);
+                a.lse[stat_at(a.bt, w.s.q0 + r, w.head[i])] = l == 0.f ? -CUDART_INF_F : m * a.scale + logf(l);
         }
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
