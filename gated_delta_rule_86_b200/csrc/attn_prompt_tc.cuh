@@ -42,10 +42,9 @@ namespace kda {
 namespace attn {
 
 constexpr int kTile = 128;   // queries of a tile, keys of a tile
-#ifndef EMU
-#define EMU 4
-#endif
-constexpr int kEmulate = EMU;  // one pair of weights in this many takes its power on the FMA units
+// One pair of weights in this many takes its powers on the FMA units.  16384 tokens, 32 heads of 128: none
+// 2.07 ms, 1 in 8 2.10, 1 in 4 2.04, 1 in 3 2.11; packed prompts, heads of 64: 272, 267, 265, 270 us.
+constexpr int kEmulate = 4;
 
 // ---- helpers shared with the gradient -----------------------------------------------------------
 
@@ -242,7 +241,7 @@ template <int D> struct FwdCfg {
 };
 
 struct FwdBars {
-    uint64_t q_full[2], full[8], empty[8], s_full[2], p_ready[2], o_full[2], drain;
+    uint64_t q_full[2], full[8], empty[8], s_full[2], p_ready[2][2], o_full[2], drain;
     uint32_t tmem;
     int abort;
     int scratch[34];
@@ -290,7 +289,8 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars.q_full[i], 1);
             tc::mbar_init(&bars.s_full[i], 1);
-            tc::mbar_init(&bars.p_ready[i], 9);   // eight softmax warps and the loads'
+            tc::mbar_init(&bars.p_ready[i][0], 9);   // eight softmax warps and the loads'
+            tc::mbar_init(&bars.p_ready[i][1], 8);
             tc::mbar_init(&bars.o_full[i], 1);
         }
         for (int i = 0; i < C::kStages; ++i) {
@@ -353,12 +353,12 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                 }
                 if (more && !(ok = warp_wait(&bars.full[kn % C::kStages], (kn / C::kStages) & 1, abort))) break;
                 if (lane == 0) {
-                    if (j < w.blocks[0]) tc::mbar_arrive(&bars.p_ready[0]);
-                    if (j < w.blocks[1]) tc::mbar_arrive(&bars.p_ready[1]);
+                    if (j < w.blocks[0]) tc::mbar_arrive(&bars.p_ready[0][0]);
+                    if (j < w.blocks[1]) tc::mbar_arrive(&bars.p_ready[1][0]);
                 }
                 // not ahead of the softmax: the next word belongs to the next turn
                 for (int i = 0; i < 2 && ok; ++i)
-                    if (j < w.blocks[i]) ok = warp_wait(&bars.p_ready[i], j & 1, abort);
+                    if (j < w.blocks[i]) ok = warp_wait(&bars.p_ready[i][0], j & 1, abort);
             }
         } else if (warp == 16 && blocks > 0) {
             constexpr uint32_t idS = tc::make_idesc_bf16(kTile, kTile, false, false);
@@ -384,10 +384,19 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (j >= w.blocks[i]) continue;
-                    if (!(ok = warp_wait(&bars.p_ready[i], j & 1, abort))) break;
-                    tc::tc_fence_after();
-                    chain_ts(tmem + kO + i * D, tmem + i * kTile, desc_mn(sbase + C::kRing + (kv % C::kStages) * C::kTileBytes, 0),
-                             idO, j > 0, leader);
+                    const uint64_t v = desc_mn(sbase + C::kRing + (kv % C::kStages) * C::kTileBytes, 0);
+#pragma unroll
+                    for (int part = 0; part < 2 && ok; ++part) {   // the first 32 columns of either half, then the rest
+                        if (!(ok = warp_wait(&bars.p_ready[i][part], j & 1, abort))) break;
+                        tc::tc_fence_after();
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int kk = (x >> 1) * 4 + part * 2 + (x & 1);
+                            mma_ts(tmem + kO + i * D, tmem + i * kTile + operand_col(kk), v + kk * 128, idO,
+                                   j > 0 || part + x > 0, leader);
+                        }
+                    }
+                    if (!ok) break;
                     if (j + 1 < w.blocks[i]) scores(i, kk1 % C::kStages);
                     else commit_by(&bars.o_full[i], leader);
                 }
@@ -489,14 +498,14 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                         u[e] = pack_bf16(y.x, y.y);
                     }
                     tc::tmem_st16(tS + c * 16, u);
+                    tc::tmem_st_wait();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bars.p_ready[i][c]);
                 }
             };
             if (masked) weights(std::false_type{});
             else weights(std::true_type{});
-            tc::tmem_st_wait();
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars.p_ready[i]);
             l += sum.x + sum.y;
         }
         if (ok && w.blocks[i] > 0) ok = warp_wait(&bars.o_full[i], 0, abort);
