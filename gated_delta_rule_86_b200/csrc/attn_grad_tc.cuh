@@ -13,8 +13,10 @@
 // S and dP are computed in both: seven products of 128 x 128 x d in place of five.  The price of the
 // second pair is less than that of adding dQ tiles to memory from every key block, and buys the fixed order.
 //
-// Warp roles: 0-7 compute (thread = row, the warpgroups take 64 columns each), 8 issues the products, 9
-// loads (TMA, and the queries' lse and delta).  P and dS are rounded once, to bf16, as operands.
+// Warp roles: 0-15 compute (thread = row, four groups of 32 columns), 16 issues the products, 17 loads
+// (TMA, and the queries' lse and delta), 18 waits for the loads on 16's behalf, zeroes rows that must not
+// count, and joins its word to the compute warps' (a wait behind products in flight returns only with
+// them).  P and dS are rounded once, to bf16, as operands.
 //
 // Rows past the end of a sequence in its last tile belong to others.  Where they are rows of a result
 // they are not stored; where they are summed over (queries in the keys' kernel, keys in the other) they
@@ -31,14 +33,16 @@ template <int D> struct GradCfg {
     static constexpr int kStages = D == 128 ? 2 : 4;      // of two tiles each
     static constexpr int kOwn = 0;                        // the block's own two tiles
     static constexpr int kRing = 2 * kTileBytes;
-    static constexpr int kStats = kRing + kStages * 2 * kTileBytes;   // lse and delta of a stage's queries
-    static constexpr int kBars = kStats + kStages * 2 * kTile * 4;
-    static constexpr int kSmem = kBars + 512 + 1024;
-    static constexpr int kThreads = 320;
+    static constexpr int kOut = kRing + kStages * 2 * kTileBytes;     // queries' kernel: the tile of O
+    static constexpr int kStats = kOut;                   // keys' kernel: -lse and -delta of a stage's queries
+    static constexpr int kBars = kOut + kTileBytes;
+    static constexpr int kSmem = kBars + 512;
+    static_assert(kStages * 2 * kTile * 4 <= kTileBytes && kSmem <= 232448, "shared memory");
+    static constexpr int kThreads = 640;
 };
 
 struct GradBars {
-    uint64_t own_full, full[4], empty[4], stats[4], s_full, dp_full[2], a_ready, b_ready, done, drain;
+    uint64_t own_full, first, full[4], empty[4], stats[4], s_full, dp_full[2], a_ready, b_ready, done, drain;
     uint32_t tmem;
     int abort;
     int scratch[34];
@@ -50,6 +54,7 @@ template <int D> __device__ __forceinline__ uint32_t grad_setup(GradBars &bars) 
     if (threadIdx.x == 0) {
         bars.abort = 0;
         tc::mbar_init(&bars.own_full, 1);
+        tc::mbar_init(&bars.first, 1);
         for (int i = 0; i < C::kStages; ++i) {
             tc::mbar_init(&bars.full[i], 1);
             tc::mbar_init(&bars.empty[i], 1);
@@ -58,13 +63,13 @@ template <int D> __device__ __forceinline__ uint32_t grad_setup(GradBars &bars) 
         tc::mbar_init(&bars.s_full, 1);
         tc::mbar_init(&bars.dp_full[0], 1);
         tc::mbar_init(&bars.dp_full[1], 1);
-        tc::mbar_init(&bars.a_ready, 8);
-        tc::mbar_init(&bars.b_ready, 8);
+        tc::mbar_init(&bars.a_ready, 17);   // sixteen compute warps and the next loads' word
+        tc::mbar_init(&bars.b_ready, 16);
         tc::mbar_init(&bars.done, 1);
         tc::mbar_init(&bars.drain, 1);
         tc::fence_mbar_init();
     }
-    if (threadIdx.x >> 5 == 8) {
+    if (threadIdx.x >> 5 == 16) {
         tc::tmem_alloc(&bars.tmem, 512);
         tc::tmem_relinquish();
     }
@@ -85,18 +90,42 @@ template <int D> __device__ __forceinline__ void drain_loads(GradBars &bars, int
     }
 }
 
-__device__ __forceinline__ void drain_products(GradBars &bars) {
-    int quit = 0;
-    tc::mma_commit(&bars.drain);
-    tc::mbar_wait(&bars.drain, 0, &quit);
+// Warp 18: for each of `total` loads, waits for it, zeroes rows from left(k) on in its first `tiles` tiles
+// where that is below 128, and passes the word on: the first by a barrier of its own, the others with
+// the compute warps' of the turn before.
+template <int D, typename F>
+__device__ __forceinline__ void watch_loads(GradBars &bars, uint8_t *ring, int total, int tiles, int lane, F left) {
+    using C = GradCfg<D>;
+    volatile int *abort = &bars.abort;
+    for (int k = 0; k <= total && total > 0; ++k) {   // the last turn has no next load to wait for
+        if (k < total) {
+            const int st = k % C::kStages, rows = left(k);
+            if (!warp_wait(&bars.full[st], (k / C::kStages) & 1, abort)) return;
+            if (rows < kTile) {
+                for (int i = 0; i < tiles; ++i) zero_rows<D>(ring + (st * 2 + i) * C::kTileBytes, rows, lane);
+                __syncwarp();
+            }
+        }
+        if (lane == 0) tc::mbar_arrive(k == 0 ? &bars.first : &bars.a_ready);
+        // the next word belongs to the next turn
+        if (k > 0 && !warp_wait(&bars.a_ready, (k - 1) & 1, abort)) return;
+    }
 }
 
-// 32 weights or score gradients of a thread's row, rounded, into Tensor Memory.
-__device__ __forceinline__ void put_operand(uint32_t taddr, const float (&x)[32]) {
+// 32 numbers of a thread's row, rounded, into Tensor Memory as an operand, over the first 16 columns of
+// the 32 that they were read from.
+__device__ __forceinline__ void put_operand(uint32_t taddr, const float2 (&x)[16]) {
     uint32_t u[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) u[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+    for (int e = 0; e < 16; ++e) u[e] = pack_bf16(x[e].x, x[e].y);
     tc::tmem_st16(taddr, u);
+}
+// d (+)= x y with x such an operand of 128 columns, y an MN-major tile.
+__device__ __forceinline__ void chain_ts32(uint32_t d, uint32_t x, uint64_t y, uint32_t idesc, bool accumulate,
+                                           uint32_t leader) {
+#pragma unroll
+    for (int kk = 0; kk < kTile / 16; ++kk)
+        mma_ts(d, x + (kk >> 1) * 32 + (kk & 1) * 8, y + kk * 128, idesc, accumulate || kk > 0, leader);
 }
 
 __device__ __forceinline__ void arrive_operand(uint64_t *bar, int lane) {
@@ -104,6 +133,23 @@ __device__ __forceinline__ void arrive_operand(uint64_t *bar, int lane) {
     tc::tc_fence_before();
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(bar);
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+
+// Gradients of rows behind the last packed sequence: zero.  Normally there are none; every block takes its share.
+template <int D> __device__ __forceinline__ void zero_behind(__nv_bfloat16 *g, const int32_t *cu, int n, int T, int heads) {
+    if (cu == nullptr) return;
+    const int from = min(max(__ldg(cu + n), 0), T);
+    const int64_t pieces = (int64_t)(T - from) * heads * (D / 8);
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * blockDim.x)
+        reinterpret_cast<uint4 *>(g + (int64_t)from * heads * D)[i] = make_uint4(0, 0, 0, 0);
 }
 
 // A warp's 32 rows of an accumulator to global memory.
@@ -132,12 +178,13 @@ template <int D>
 __global__ void __launch_bounds__(GradCfg<D>::kThreads, 1)
 attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps) {
     using C = GradCfg<D>;
-    extern __shared__ uint8_t raw[];
-    uint8_t *smem = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     GradBars &bars = *reinterpret_cast<GradBars *>(smem + C::kBars);
     const uint32_t sbase = tc::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    zero_behind<D>(static_cast<__nv_bfloat16 *>(a.dk), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv);
+    zero_behind<D>(static_cast<__nv_bfloat16 *>(a.dv), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv);
     // the first keys of a sequence are seen by the most queries: they go first
     int n, t;
     if (!find_tile(a.bt.cu_k, a.bt.n, a.bt.Tk, kTile, blockIdx.x / a.bt.Hkv, bars.scratch, n, t)) return;
@@ -152,7 +199,7 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
     const uint32_t tS = tmem, tP = tmem + kTile, tV = tmem + 2 * kTile, tK = tV + D;
     float *stats = reinterpret_cast<float *>(smem + C::kStats);
 
-    if (warp == 9) {
+    if (warp == 17) {
         if (total > 0) {
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(&bars.own_full, 2 * C::kTileBytes);
@@ -163,18 +210,18 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
             int put = 0;
             for (int it = 0; it < total; ++it) {
                 const int st = it % C::kStages, h = hk * group + it / per_head, r0 = (start + it % per_head) * kTile;
-                // lse in log2 units, +inf (weight zero) where there is no query or it sees nothing
+                // -lse in log2 units, -inf (weight zero) where there is no query or it sees nothing; -delta
                 float ls[4], de[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int r = r0 + e * 32 + lane;
-                    ls[e] = CUDART_INF_F;
+                    ls[e] = -CUDART_INF_F;
                     de[e] = 0.f;
                     if (r < s.nq) {
                         const int64_t at = stat_at(a.bt, s.q0 + r, h);
                         const float x = a.lse[at] * kLog2e;
-                        ls[e] = x == -CUDART_INF_F ? CUDART_INF_F : x;
-                        de[e] = a.delta[at];
+                        ls[e] = x == -CUDART_INF_F ? x : -x;
+                        de[e] = -a.delta[at];
                     }
                 }
                 if (it >= C::kStages) ok = warp_wait(&bars.empty[st], (it / C::kStages - 1) & 1, abort);
@@ -196,151 +243,143 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
             }
             if (!ok && lane == 0) drain_loads<D>(bars, put);
         }
-    } else if (warp == 8) {
+    } else if (warp == 18) {
+        // queries that are not there are summed over with weight zero
+        watch_loads<D>(bars, smem + C::kRing, total, 2, lane,
+                       [&](int k) { return s.nq - (start + k % per_head) * kTile; });
+    } else if (warp == 16) {
         constexpr uint32_t idS = tc::make_idesc_bf16(kTile, kTile, false, false);
         constexpr uint32_t idG = tc::make_idesc_bf16(kTile, D, false, true);
-        bool ok = true;
-        auto load_ready = [&](int it) {
-            const int st = it % C::kStages;
-            if (!warp_wait(&bars.full[st], (it / C::kStages) & 1, abort)) return false;
-            const int left = s.nq - (start + it % per_head) * kTile;
-            if (left < kTile) {   // queries that are not there are summed over with weight zero
-                zero_rows<D>(smem + C::kRing + st * 2 * C::kTileBytes, left, lane);
-                zero_rows<D>(smem + C::kRing + st * 2 * C::kTileBytes + C::kTileBytes, left, lane);
-                __syncwarp();
-            }
-            return true;
-        };
-        auto product = [&](uint32_t d, uint32_t x, uint32_t y, uint64_t *bar) {   // d = x y^T
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) tc::mma_f16(d, desc_k(x, kk), desc_k(y, kk), idS, kk > 0);
-            tc::mma_commit(bar);
-        };
+        const uint32_t leader = elect_lane();
         const uint32_t sK = sbase + C::kOwn, sV = sK + C::kTileBytes;
+        bool ok = true;
         if (total > 0) {
-            ok = warp_wait(&bars.own_full, 0, abort) && load_ready(0);
-            if (ok && lane == 0) {
-                product(tS, sK, sbase + C::kRing, &bars.s_full);
-                product(tP, sV, sbase + C::kRing + C::kTileBytes, &bars.dp_full[0]);
+            ok = warp_wait(&bars.own_full, 0, abort) && warp_wait(&bars.first, 0, abort);
+            if (ok) {
+                chain_ss<D>(tS, desc_k(sK, 0), desc_k(sbase + C::kRing, 0), idS, leader);
+                commit_by(&bars.s_full, leader);
+                chain_ss<D>(tP, desc_k(sV, 0), desc_k(sbase + C::kRing + C::kTileBytes, 0), idS, leader);
+                commit_by(&bars.dp_full[0], leader);
             }
         }
         for (int it = 0; it < total && ok; ++it) {
             const uint32_t q = sbase + C::kRing + (it % C::kStages) * 2 * C::kTileBytes, g = q + C::kTileBytes;
             const uint32_t qn = sbase + C::kRing + ((it + 1) % C::kStages) * 2 * C::kTileBytes;
             const bool more = it + 1 < total;
-            if (more && !(ok = load_ready(it + 1))) break;
             if (!(ok = warp_wait(&bars.a_ready, it & 1, abort))) break;
             tc::tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                    tc::mma_f16_ta(tV, tS + operand_col(kk), desc_mn(g, kk), idG, it > 0 || kk > 0);
-                if (more) product(tS, sK, qn, &bars.s_full);
+            chain_ts32(tV, tS, desc_mn(g, 0), idG, it > 0, leader);
+            if (more) {
+                chain_ss<D>(tS, desc_k(sK, 0), desc_k(qn, 0), idS, leader);
+                commit_by(&bars.s_full, leader);
             }
             if (!(ok = warp_wait(&bars.b_ready, it & 1, abort))) break;
             tc::tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                    tc::mma_f16_ta(tK, tP + operand_col(kk), desc_mn(q, kk), idG, it > 0 || kk > 0);
-                tc::mma_commit(more ? &bars.empty[it % C::kStages] : &bars.done);
-                if (more) product(tP, sV, qn + C::kTileBytes, &bars.dp_full[0]);
+            chain_ts32(tK, tP, desc_mn(q, 0), idG, it > 0, leader);
+            if (more) {
+                chain_ss<D>(tP, desc_k(sV, 0), desc_k(qn + C::kTileBytes, 0), idS, leader);
+                commit_by(&bars.dp_full[0], leader);
             }
+            commit_by(more ? &bars.empty[it % C::kStages] : &bars.done, leader);
         }
-        if (!ok && lane == 0) drain_products(bars);
-        __syncwarp();
-    } else {
-        const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
-        const uint32_t lanes = tc::tmem_lane_base(warp);
+        if (!ok) {   // no product in flight when the memory is given back
+            int quit = 0;
+            commit_by(&bars.drain, leader);
+            warp_wait(&bars.drain, 0, &quit);
+        }
+    } else if (warp < 16) {
+        const int part = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tc::tmem_lane_base(warp) + part * 32;
         const float sc = a.scale * kLog2e;
+        const float2 sc2 = make_float2(sc, sc);
         bool ok = true;
         for (int it = 0; it < total; ++it) {
-            const int st = it % C::kStages, r0 = (start + it % per_head) * kTile;
-            const float *ls = stats + st * 2 * kTile + wg * 64, *de = ls + kTile;
+            const int st = it % C::kStages, r0 = (start + it % per_head) * kTile + part * 32;
+            const float *ls = stats + st * 2 * kTile + part * 32, *de = ls + kTile;
             // this row's key is seen by the tile's queries from column `from` on
-            const int from = a.causal ? c0 + row - ahead - r0 - wg * 64 : 0;
-            const bool partly = a.causal && c0 + (warp & 3) * 32 + 31 - ahead - r0 - wg * 64 > 0;
+            const int from = c0 + row - ahead - r0;
+            const bool partly = a.causal && c0 + (warp & 3) * 32 + 31 - ahead - r0 > 0;
             ok = warp_wait(&bars.stats[st], (it / C::kStages) & 1, abort) && warp_wait(&bars.s_full, it & 1, abort);
             if (!ok) break;
             tc::tc_fence_after();
-            float p[2][32];
+            float2 p[16];
+            {
+                float x[32];
+                tc::tmem_ld32(tS + lanes, x);
+                tc::tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tc::tmem_ld32(tS + lanes + wg * 64 + c * 32, p[c]);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 l4 = *reinterpret_cast<const float4 *>(ls + c * 32 + e);
-                    p[c][e] = ex2_approx(fmaf(p[c][e], sc, -l4.x));
-                    p[c][e + 1] = ex2_approx(fmaf(p[c][e + 1], sc, -l4.y));
-                    p[c][e + 2] = ex2_approx(fmaf(p[c][e + 2], sc, -l4.z));
-                    p[c][e + 3] = ex2_approx(fmaf(p[c][e + 3], sc, -l4.w));
+                for (int e = 0; e < 16; e += 2) {
+                    const float4 l4 = *reinterpret_cast<const float4 *>(ls + 2 * e);
+                    p[e] = fma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, make_float2(l4.x, l4.y));
+                    p[e + 1] = fma2(make_float2(x[2 * e + 2], x[2 * e + 3]), sc2, make_float2(l4.z, l4.w));
                 }
-                if (partly) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c * 32 + e < from) p[c][e] = 0.f;
-                }
-                put_operand(tS + lanes + wg * 64 + c * 16, p[c]);
             }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) p[e] = make_float2(ex2_approx(p[e].x), ex2_approx(p[e].y));
+            if (partly) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if (2 * e < from) p[e].x = 0.f;
+                    if (2 * e + 1 < from) p[e].y = 0.f;
+                }
+            }
+            put_operand(tS + lanes, p);
             arrive_operand(&bars.a_ready, lane);
             ok = warp_wait(&bars.dp_full[0], it & 1, abort);
             if (!ok) break;
             tc::tc_fence_after();
-            float x[2][32];
+            {
+                float x[32];
+                tc::tmem_ld32(tP + lanes, x);
+                tc::tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tc::tmem_ld32(tP + lanes + wg * 64 + c * 32, x[c]);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 d4 = *reinterpret_cast<const float4 *>(de + c * 32 + e);
-                    x[c][e] = p[c][e] * (x[c][e] - d4.x);
-                    x[c][e + 1] = p[c][e + 1] * (x[c][e + 1] - d4.y);
-                    x[c][e + 2] = p[c][e + 2] * (x[c][e + 2] - d4.z);
-                    x[c][e + 3] = p[c][e + 3] * (x[c][e + 3] - d4.w);
+                for (int e = 0; e < 16; e += 2) {
+                    const float4 d4 = *reinterpret_cast<const float4 *>(de + 2 * e);
+                    p[e] = mul2(p[e], add2(make_float2(x[2 * e], x[2 * e + 1]), make_float2(d4.x, d4.y)));
+                    p[e + 1] = mul2(p[e + 1], add2(make_float2(x[2 * e + 2], x[2 * e + 3]), make_float2(d4.z, d4.w)));
                 }
-                if (partly) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c * 32 + e < from) x[c][e] = 0.f;
-                }
-                put_operand(tP + lanes + wg * 64 + c * 16, x[c]);
             }
+            if (partly) {   // a hidden query's dP may be anything
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if (2 * e < from) p[e].x = 0.f;
+                    if (2 * e + 1 < from) p[e].y = 0.f;
+                }
+            }
+            put_operand(tP + lanes, p);
             arrive_operand(&bars.b_ready, lane);
         }
         if (ok && total > 0) ok = warp_wait(&bars.done, 0, abort);
-        if (ok) {
+        if (ok && part < 2) {
             tc::tc_fence_after();
-            // one warpgroup writes dV, the other dK, through the tiles of K and V, which are done with
-            const int r0 = c0 + (warp & 3) * 32;
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(wg ? a.dk : a.dv) + ((s.k0 + r0) * a.bt.Hkv + hk) * D;
-            store_rows<D>((wg ? tK : tV) + lanes, smem + C::kOwn + wg * C::kTileBytes + (warp & 3) * 32 * D * 2, lane,
-                          dst, (int64_t)a.bt.Hkv * D, s.nk - r0, wg ? a.scale : 1.f, total == 0);
+            // one warpgroup writes dV, another dK, through the tiles of K and V, which are done with
+            const int k0 = c0 + (warp & 3) * 32;
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(part ? a.dk : a.dv) + ((s.k0 + k0) * a.bt.Hkv + hk) * D;
+            store_rows<D>((part ? tK : tV) + tc::tmem_lane_base(warp),
+                          smem + C::kOwn + part * C::kTileBytes + (warp & 3) * 32 * D * 2, lane, dst,
+                          (int64_t)a.bt.Hkv * D, s.nk - k0, part ? a.scale : 1.f, total == 0);
         }
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
 }
 
-// ---- dQ -----------------------------------------------------------------------------------------
+// ---- dQ, and delta for the keys' kernel ---------------------------------------------------------
 
 template <int D>
 __global__ void __launch_bounds__(GradCfg<D>::kThreads, 1)
 attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps) {
     using C = GradCfg<D>;
-    extern __shared__ uint8_t raw[];
-    uint8_t *smem = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     GradBars &bars = *reinterpret_cast<GradBars *>(smem + C::kBars);
     const uint32_t sbase = tc::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    zero_behind<D>(static_cast<__nv_bfloat16 *>(a.dq), a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq);
     const int64_t tiles = gridDim.x / a.bt.Hq;
     int n, t;
     if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, kTile, tiles - 1 - blockIdx.x / a.bt.Hq, bars.scratch, n, t)) return;
@@ -352,11 +391,12 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
     volatile int *abort = &bars.abort;
     const uint32_t tS = tmem, tP = tmem + kTile, tQ = tmem + 3 * kTile;
 
-    if (warp == 9) {
-        if (lane == 0 && total > 0) {
-            tc::mbar_arrive_expect_tx(&bars.own_full, 2 * C::kTileBytes);
+    if (warp == 17) {
+        if (lane == 0) {
+            tc::mbar_arrive_expect_tx(&bars.own_full, 3 * C::kTileBytes);
             tma_tile<D>(C::kOwn, smem, &maps.q, h, s.q0 + r0, &bars.own_full);
             tma_tile<D>(C::kOwn + C::kTileBytes, smem, &maps.g, h, s.q0 + r0, &bars.own_full);
+            tma_tile<D>(C::kOut, smem, &maps.o, h, s.q0 + r0, &bars.own_full);
             bool ok = true;
             int put = 0;
             for (int j = 0; j < total; ++j) {
@@ -371,113 +411,117 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
             }
             if (!ok) drain_loads<D>(bars, put);
         }
-    } else if (warp == 8) {
+    } else if (warp == 18) {
+        // keys that are not there are summed over with weight zero (their values only masked)
+        watch_loads<D>(bars, smem + C::kRing, total, 1, lane, [&](int k) { return s.nk - k * kTile; });
+    } else if (warp == 16) {
         constexpr uint32_t idS = tc::make_idesc_bf16(kTile, kTile, false, false);
         constexpr uint32_t idG = tc::make_idesc_bf16(kTile, D, false, true);
-        bool ok = true;
-        auto load_ready = [&](int j) {
-            const int st = j % C::kStages;
-            if (!warp_wait(&bars.full[st], (j / C::kStages) & 1, abort)) return false;
-            const int left = s.nk - j * kTile;
-            if (left < kTile) {   // keys that are not there are summed over with weight zero
-                zero_rows<D>(smem + C::kRing + st * 2 * C::kTileBytes, left, lane);
-                __syncwarp();
-            }
-            return true;
-        };
-        auto product = [&](uint32_t d, uint32_t x, uint32_t y, uint64_t *bar) {   // d = x y^T
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) tc::mma_f16(d, desc_k(x, kk), desc_k(y, kk), idS, kk > 0);
-            tc::mma_commit(bar);
-        };
+        const uint32_t leader = elect_lane();
         const uint32_t sQ = sbase + C::kOwn, sG = sQ + C::kTileBytes;
+        bool ok = true;
         if (total > 0) {
-            ok = warp_wait(&bars.own_full, 0, abort) && load_ready(0);
-            if (ok && lane == 0) {
-                product(tS, sQ, sbase + C::kRing, &bars.s_full);
-                product(tP, sG, sbase + C::kRing + C::kTileBytes, &bars.dp_full[0]);
+            ok = warp_wait(&bars.own_full, 0, abort) && warp_wait(&bars.first, 0, abort);
+            if (ok) {
+                chain_ss<D>(tS, desc_k(sQ, 0), desc_k(sbase + C::kRing, 0), idS, leader);
+                commit_by(&bars.s_full, leader);
+                chain_ss<D>(tP, desc_k(sG, 0), desc_k(sbase + C::kRing + C::kTileBytes, 0), idS, leader);
+                commit_by(&bars.dp_full[0], leader);
             }
         }
         for (int j = 0; j < total && ok; ++j) {
             const uint32_t k = sbase + C::kRing + (j % C::kStages) * 2 * C::kTileBytes;
             const uint32_t kn = sbase + C::kRing + ((j + 1) % C::kStages) * 2 * C::kTileBytes;
             const bool more = j + 1 < total;
-            if (more) {
-                // the next scores as soon as these have been read; dP alternates between two places
-                if (!(ok = load_ready(j + 1))) break;
+            if (more) {   // the next scores as soon as these have been read; dP alternates between two places
                 if (!(ok = warp_wait(&bars.a_ready, j & 1, abort))) break;
                 tc::tc_fence_after();
-                if (lane == 0) {
-                    product(tS, sQ, kn, &bars.s_full);
-                    product(tP + ((j + 1) & 1) * kTile, sG, kn + C::kTileBytes, &bars.dp_full[(j + 1) & 1]);
-                }
+                chain_ss<D>(tS, desc_k(sQ, 0), desc_k(kn, 0), idS, leader);
+                commit_by(&bars.s_full, leader);
+                chain_ss<D>(tP + ((j + 1) & 1) * kTile, desc_k(sG, 0), desc_k(kn + C::kTileBytes, 0), idS, leader);
+                commit_by(&bars.dp_full[(j + 1) & 1], leader);
             }
             if (!(ok = warp_wait(&bars.b_ready, j & 1, abort))) break;
             tc::tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                    tc::mma_f16_ta(tQ, tP + (j & 1) * kTile + operand_col(kk), desc_mn(k, kk), idG, j > 0 || kk > 0);
-                tc::mma_commit(more ? &bars.empty[j % C::kStages] : &bars.done);
-            }
+            chain_ts32(tQ, tP + (j & 1) * kTile, desc_mn(k, 0), idG, j > 0, leader);
+            commit_by(more ? &bars.empty[j % C::kStages] : &bars.done, leader);
         }
-        if (!ok && lane == 0) drain_products(bars);
-        __syncwarp();
-    } else {
-        const int wg = warp >> 2, row = (warp & 3) * 32 + lane, r = r0 + row;
-        const uint32_t lanes = tc::tmem_lane_base(warp);
+        if (!ok) {   // no product in flight when the memory is given back
+            int quit = 0;
+            commit_by(&bars.drain, leader);
+            warp_wait(&bars.drain, 0, &quit);
+        }
+    } else if (warp < 16) {
+        const int part = warp >> 2, row = (warp & 3) * 32 + lane, r = r0 + row;
+        const uint32_t lanes = tc::tmem_lane_base(warp) + part * 32;
         const float sc = a.scale * kLog2e;
         const int seen = r < s.nq ? keys_seen(s, r, a.causal) : 0;
         const int first_row = r0 + (warp & 3) * 32;
         const int seen_all = first_row + 31 < s.nq ? keys_seen(s, first_row, a.causal) : 0;   // by every row of the warp
-        float ls = CUDART_INF_F, de = 0.f;
+        float ls = -CUDART_INF_F;
+        const int64_t at = r < s.nq ? stat_at(a.bt, s.q0 + r, h) : 0;
         if (r < s.nq) {
-            const int64_t at = stat_at(a.bt, s.q0 + r, h);
             ls = a.lse[at] * kLog2e;
-            if (ls == -CUDART_INF_F) ls = CUDART_INF_F;
-            de = a.delta[at];
+            if (ls != -CUDART_INF_F) ls = -ls;
         }
-        bool ok = true;
-        for (int j = 0; j < total; ++j) {
-            const uint32_t dp = tP + (j & 1) * kTile + lanes + wg * 64;
-            const int limit = seen - j * kTile - wg * 64;   // columns at or past it are hidden
-            const bool partly = j * kTile + kTile > seen_all;
-            ok = warp_wait(&bars.s_full, j & 1, abort);
-            if (!ok) break;
-            tc::tc_fence_after();
-            float p[2][32];
+        bool ok = warp_wait(&bars.own_full, 0, abort);
+        float de = 0.f;
+        if (ok) {   // delta = dO . O of this row, the same in all four groups
+            const uint8_t *g = smem + C::kOwn + C::kTileBytes, *o = smem + C::kOut;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tc::tmem_ld32(tS + lanes + wg * 64 + c * 32, p[c]);
-            tc::tmem_ld_wait();
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars.a_ready);
+            for (int c = 0; c < D / 8; ++c) {
+                const uint32_t off = (c >> 3) * (kTile * 128) + tc::sw128(row, c & 7);
+                const uint4 x = *reinterpret_cast<const uint4 *>(g + off), y = *reinterpret_cast<const uint4 *>(o + off);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) p[c][e] = ex2_approx(fmaf(p[c][e], sc, -ls));
-            ok = warp_wait(&bars.dp_full[j & 1], (j >> 1) & 1, abort);
-            if (!ok) break;
-            tc::tc_fence_after();
-            float x[2][32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) tc::tmem_ld32(dp + c * 32, x[c]);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[c][e] = p[c][e] * (x[c][e] - de);
-                if (partly) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c * 32 + e >= limit) x[c][e] = 0.f;
+                for (int e = 0; e < 4; ++e) {
+                    de = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), de);
+                    de = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), de);
                 }
-                put_operand(dp + c * 16, x[c]);
             }
+            if (part == 0 && r < s.nq) a.delta[at] = de;
+        }
+        const float2 sc2 = make_float2(sc, sc), ls2 = make_float2(ls, ls), de2 = make_float2(-de, -de);
+        for (int j = 0; j < total && ok; ++j) {
+            const uint32_t dp = tP + (j & 1) * kTile + lanes;
+            const int limit = seen - j * kTile - part * 32;   // columns at or past it are hidden
+            const bool partly = j * kTile + (part + 1) * 32 > seen_all;
+            if (!(ok = warp_wait(&bars.s_full, j & 1, abort))) break;
+            tc::tc_fence_after();
+            float2 p[16];
+            {
+                float x[32];
+                tc::tmem_ld32(tS + lanes, x);
+                tc::tmem_ld_wait();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars.a_ready);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) p[e] = fma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, ls2);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) p[e] = make_float2(ex2_approx(p[e].x), ex2_approx(p[e].y));
+            if (!(ok = warp_wait(&bars.dp_full[j & 1], (j >> 1) & 1, abort))) break;
+            tc::tc_fence_after();
+            {
+                float x[32];
+                tc::tmem_ld32(dp, x);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) p[e] = mul2(p[e], add2(make_float2(x[2 * e], x[2 * e + 1]), de2));
+            }
+            if (partly) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if (2 * e >= limit) p[e].x = 0.f;
+                    if (2 * e + 1 >= limit) p[e].y = 0.f;
+                }
+            }
+            put_operand(dp, p);
             arrive_operand(&bars.b_ready, lane);
         }
         if (ok && total > 0) ok = warp_wait(&bars.done, 0, abort);
-        if (ok && wg == 0) {
+        if (ok && part == 0) {
             tc::tc_fence_after();
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.dq) + ((s.q0 + first_row) * a.bt.Hq + h) * D;
             store_rows<D>(tQ + lanes, smem + C::kOwn + (warp & 3) * 32 * D * 2, lane, dst, (int64_t)a.bt.Hq * D,
@@ -486,7 +530,7 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
@@ -494,21 +538,22 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
 
 template <int D> cudaError_t launch_prompt_grad_tc(const PromptArgs &a, cudaStream_t st) {
     using C = GradCfg<D>;
-    cudaError_t e = launch_delta<__nv_bfloat16, D>(a, st);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     const int64_t gk = a.bt.Tk == 0 ? 0 : max_tiles(a.bt.cu_k, a.bt.n, a.bt.Tk, kTile) * a.bt.Hkv;
     const int64_t gq = a.bt.Tq == 0 ? 0 : max_tiles(a.bt.cu_q, a.bt.n, a.bt.Tq, kTile) * a.bt.Hq;
     if (gk > 0x7fffffff || gq > 0x7fffffff) return cudaErrorInvalidValue;
+    // before the maps: it binds the device's context to this thread (autograd's may have none yet), which
+    // their encoding needs
+    if ((e = allow_smem(attn_grad_q_tc_kernel<D>, C::kSmem)) != cudaSuccess) return e;
     PromptMaps maps = {};
     if (a.bt.Tq > 0 && !encode_prompt_maps(maps, a, D)) return cudaErrorInvalidValue;
+    if (gq > 0) {   // first: it forms the delta that the other reads
+        attn_grad_q_tc_kernel<D><<<(unsigned)gq, C::kThreads, C::kSmem, st>>>(a, maps);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
     if (gk > 0) {
         if ((e = allow_smem(attn_grad_kv_tc_kernel<D>, C::kSmem)) != cudaSuccess) return e;
         attn_grad_kv_tc_kernel<D><<<(unsigned)gk, C::kThreads, C::kSmem, st>>>(a, maps);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    if (gq > 0) {
-        if ((e = allow_smem(attn_grad_q_tc_kernel<D>, C::kSmem)) != cudaSuccess) return e;
-        attn_grad_q_tc_kernel<D><<<(unsigned)gq, C::kThreads, C::kSmem, st>>>(a, maps);
     }
     return cudaGetLastError();
 }

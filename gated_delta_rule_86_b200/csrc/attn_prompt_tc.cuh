@@ -223,7 +223,7 @@ template <int D> struct RowWriter {
 // ---- forward ------------------------------------------------------------------------------------
 
 struct PromptMaps {
-    CUtensorMap q, k, v, g;   // g: d_out (gradient only)
+    CUtensorMap q, k, v, g, o;   // g, o: d_out and out (gradient only)
 };
 
 template <int D> struct FwdCfg {
@@ -569,7 +569,8 @@ inline bool encode_prompt_maps(PromptMaps &m, const PromptArgs &a, int d) {
     return encode_tile_map(&m.q, a.q, a.q_stride, d, a.bt.Hq, tq) &&
            (tk == 0 || (encode_tile_map(&m.k, a.k, a.k_stride, d, a.bt.Hkv, tk) &&
                         encode_tile_map(&m.v, a.v, a.v_stride, d, a.bt.Hkv, tk))) &&
-           (!a.d_out || encode_tile_map(&m.g, a.d_out, (int64_t)a.bt.Hq * d, d, a.bt.Hq, tq));
+           (!a.d_out || (encode_tile_map(&m.g, a.d_out, (int64_t)a.bt.Hq * d, d, a.bt.Hq, tq) &&
+                         encode_tile_map(&m.o, a.out, (int64_t)a.bt.Hq * d, d, a.bt.Hq, tq)));
 }
 
 template <int D> cudaError_t launch_prompt_tc(const PromptArgs &a, cudaStream_t st) {
@@ -580,10 +581,11 @@ template <int D> cudaError_t launch_prompt_tc(const PromptArgs &a, cudaStream_t 
     const int64_t grid = tiles * (pair ? a.bt.Hq / 2 : a.bt.Hq);
     if (a.bt.Tq == 0 || grid == 0) return cudaSuccess;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    PromptMaps maps = {};
-    if (!encode_prompt_maps(maps, a, D)) return cudaErrorInvalidValue;
+    // before the maps: it binds the device's context to this thread, which their encoding needs
     const cudaError_t e = allow_smem(attn_prompt_tc_kernel<D>, C::kSmem);
     if (e != cudaSuccess) return e;
+    PromptMaps maps = {};
+    if (!encode_prompt_maps(maps, a, D)) return cudaErrorInvalidValue;
     attn_prompt_tc_kernel<D><<<(unsigned)grid, C::kThreads, C::kSmem, st>>>(a, maps, pair);
     return cudaGetLastError();
 }

@@ -1,6 +1,7 @@
 """Softmax attention on the GPU: prompts and their gradient, the paged cache's append and decode step,
 each against the definitions in 64 bits (oracle/attention.py) within bounds that count every rounding."""
 import math
+import threading
 
 import pytest
 import torch
@@ -572,3 +573,25 @@ def test_other_streams():
             got.append(kda.kda_attn_fwd(q, k, v, cu))
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for x in got)
+
+
+def test_fresh_threads():
+    """Every call as the first of its thread, where no CUDA context is bound yet."""
+    q, k, v, cu, _ = prompt("packed", 4, 2, 128, BF16, seed=710)
+    g = make(q.shape, 715, BF16)
+    out, lse = kda.kda_attn_fwd(q, k, v, cu, return_lse=True)
+    want = kda.kda_attn_bwd(q, k, v, out, lse, g, cu)
+    kc, vc, table = cache_of([40], 2, 128, 16, BF16, 720)
+    seq = torch.tensor([40], dtype=torch.int32, device="cuda")
+    dec = kda.kda_attn_decode_step(q[:, 0], kc, vc, table, seq)
+    torch.cuda.synchronize()
+    got, calls = {}, dict(
+        fwd=lambda: kda.kda_attn_fwd(q, k, v, cu), bwd=lambda: kda.kda_attn_bwd(q, k, v, out, lse, g, cu),
+        dec=lambda: kda.kda_attn_decode_step(q[:, 0], kc, vc, table, seq))
+    for name, call in calls.items():
+        t = threading.Thread(target=lambda: got.__setitem__(name, call()))
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert torch.equal(got["fwd"], out) and torch.equal(got["dec"], dec)
+    assert all(torch.equal(a, b) for a, b in zip(got["bwd"], want))
