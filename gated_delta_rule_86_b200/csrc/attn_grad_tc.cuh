@@ -30,41 +30,48 @@ namespace attn {
 
 template <int D> struct GradCfg {
     static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kStages = D == 128 ? 2 : 4;      // of two tiles each
+    static constexpr int kStages = D == 128 ? 5 : 8;      // of one tile each, released one by one
     static constexpr int kOwn = 0;                        // the block's own two tiles
     static constexpr int kRing = 2 * kTileBytes;
-    static constexpr int kOut = kRing + kStages * 2 * kTileBytes;     // queries' kernel: the tile of O
-    static constexpr int kStats = kOut;                   // keys' kernel: -lse and -delta of a stage's queries
-    static constexpr int kBars = kOut + kTileBytes;
+    static constexpr int kOut = kRing + (kStages - 1) * kTileBytes;   // queries' kernel: O, in the last stage at first
+    static constexpr int kStats = kRing + kStages * kTileBytes;       // keys' kernel: -lse and -delta of two turns' queries
+    static constexpr int kBars = kStats + 2 * 2 * kTile * 4;
     static constexpr int kSmem = kBars + 512;
-    static_assert(kStages * 2 * kTile * 4 <= kTileBytes && kSmem <= 232448, "shared memory");
+    static_assert(kSmem <= 232448, "shared memory");
     static constexpr int kThreads = 640;
 };
 
 struct GradBars {
-    uint64_t own_full, first, full[4], empty[4], stats[4], s_full, dp_full[2], a_ready, b_ready, done, drain;
+    uint64_t own_full, out_full, out_read, first, full[8], empty[8], stats[2], stats_read[2], s_full, dp_full[2], a_ready,
+        b_ready, done, drain;
     uint32_t tmem;
     int abort;
     int scratch[34];
 };
+static_assert(sizeof(GradBars) <= 512, "barriers");
 
 // Barriers and Tensor Memory; every thread.  Returns the Tensor Memory's base.
-template <int D> __device__ __forceinline__ uint32_t grad_setup(GradBars &bars) {
+template <int D> __device__ __forceinline__ uint32_t grad_setup(GradBars &bars, int b_count) {
     using C = GradCfg<D>;
     if (threadIdx.x == 0) {
         bars.abort = 0;
         tc::mbar_init(&bars.own_full, 1);
         tc::mbar_init(&bars.first, 1);
+        tc::mbar_init(&bars.out_full, 1);
+        tc::mbar_init(&bars.out_read, 16);
         for (int i = 0; i < C::kStages; ++i) {
             tc::mbar_init(&bars.full[i], 1);
             tc::mbar_init(&bars.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars.stats[i], 1);
+            tc::mbar_init(&bars.stats_read[i], 16);
         }
         tc::mbar_init(&bars.s_full, 1);
         tc::mbar_init(&bars.dp_full[0], 1);
         tc::mbar_init(&bars.dp_full[1], 1);
         tc::mbar_init(&bars.a_ready, 17);   // sixteen compute warps and the next loads' word
-        tc::mbar_init(&bars.b_ready, 16);
+        tc::mbar_init(&bars.b_ready, b_count);
         tc::mbar_init(&bars.done, 1);
         tc::mbar_init(&bars.drain, 1);
         tc::fence_mbar_init();
@@ -79,37 +86,46 @@ template <int D> __device__ __forceinline__ uint32_t grad_setup(GradBars &bars) 
     return bars.tmem;
 }
 
-// After a wait that ran out: waits for the loads of the last `stages` puts, so that none is in flight.
-template <int D> __device__ __forceinline__ void drain_loads(GradBars &bars, int put) {
+// Load number k, counted from the first, lies in stage k mod kStages.
+template <int D> __device__ __forceinline__ uint32_t stage_of(int k) {
+    return GradCfg<D>::kRing + (k % GradCfg<D>::kStages) * GradCfg<D>::kTileBytes;
+}
+
+// Warp 17's lane: loads `total` pairs of tiles, pair(k, bar, at) issuing tile k & 1 of pair k >> 1.  The
+// last stage's first filling waits for `hold`, if given.
+template <int D, typename F>
+__device__ __forceinline__ void load_ring(GradBars &bars, int total, uint64_t *hold, F issue) {
     using C = GradCfg<D>;
-    int quit = 0;
-    tc::mbar_wait(&bars.own_full, 0, &quit);
-    for (int k = put > C::kStages ? put - C::kStages : 0; k < put; ++k) {
-        quit = 0;
-        tc::mbar_wait(&bars.full[k % C::kStages], (k / C::kStages) & 1, &quit);
+    volatile int *abort = &bars.abort;
+    bool ok = true;
+    int k = 0;
+    for (; k < 2 * total; ++k) {
+        const int st = k % C::kStages;
+        if (k >= C::kStages) ok = tc::mbar_wait(&bars.empty[st], (k / C::kStages - 1) & 1, abort);
+        else if (hold && k == C::kStages - 1) ok = tc::mbar_wait(hold, 0, abort);
+        if (!ok) break;
+        tc::mbar_arrive_expect_tx(&bars.full[st], C::kTileBytes);
+        issue(k, stage_of<D>(k), &bars.full[st]);
+    }
+    if (!ok) {   // a wait ran out: leave no copy in flight
+        int quit = 0;
+        tc::mbar_wait(&bars.own_full, 0, &quit);
+        for (int i = k > C::kStages ? k - C::kStages : 0; i < k; ++i) {
+            quit = 0;
+            tc::mbar_wait(&bars.full[i % C::kStages], (i / C::kStages) & 1, &quit);
+        }
     }
 }
 
-// Warp 18: for each of `total` loads, waits for it, zeroes rows from left(k) on in its first `tiles` tiles
-// where that is below 128, and passes the word on: the first by a barrier of its own, the others with
-// the compute warps' of the turn before.
-template <int D, typename F>
-__device__ __forceinline__ void watch_loads(GradBars &bars, uint8_t *ring, int total, int tiles, int lane, F left) {
+// Warp 18: waits for load k and zeroes its rows from `rows` on, where that is below 128.
+template <int D> __device__ __forceinline__ bool watch_load(GradBars &bars, uint8_t *smem, int k, int rows, int lane) {
     using C = GradCfg<D>;
-    volatile int *abort = &bars.abort;
-    for (int k = 0; k <= total && total > 0; ++k) {   // the last turn has no next load to wait for
-        if (k < total) {
-            const int st = k % C::kStages, rows = left(k);
-            if (!warp_wait(&bars.full[st], (k / C::kStages) & 1, abort)) return;
-            if (rows < kTile) {
-                for (int i = 0; i < tiles; ++i) zero_rows<D>(ring + (st * 2 + i) * C::kTileBytes, rows, lane);
-                __syncwarp();
-            }
-        }
-        if (lane == 0) tc::mbar_arrive(k == 0 ? &bars.first : &bars.a_ready);
-        // the next word belongs to the next turn
-        if (k > 0 && !warp_wait(&bars.a_ready, (k - 1) & 1, abort)) return;
+    if (!warp_wait(&bars.full[k % C::kStages], (k / C::kStages) & 1, &bars.abort)) return false;
+    if (rows < kTile) {
+        zero_rows<D>(smem + stage_of<D>(k), rows, lane);
+        __syncwarp();
     }
+    return true;
 }
 
 // 32 numbers of a thread's row, rounded, into Tensor Memory as an operand, over the first 16 columns of
@@ -194,59 +210,74 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
     const int start = a.causal ? max(0, c0 - ahead) / kTile : 0;
     const int per_head = max(0, (s.nq + kTile - 1) / kTile - start), total = per_head * group;
 
-    const uint32_t tmem = grad_setup<D>(bars);
+    const uint32_t tmem = grad_setup<D>(bars, 17);
     volatile int *abort = &bars.abort;
     const uint32_t tS = tmem, tP = tmem + kTile, tV = tmem + 2 * kTile, tK = tV + D;
     float *stats = reinterpret_cast<float *>(smem + C::kStats);
+    // turn `it` is query tile r0 of head h; its Q is load 2 it, its dO load 2 it + 1
+    auto head_of = [&](int it) { return hk * group + it / per_head; };
+    auto row_of = [&](int it) { return (start + it % per_head) * kTile; };
 
     if (warp == 17) {
-        if (total > 0) {
-            if (lane == 0) {
-                tc::mbar_arrive_expect_tx(&bars.own_full, 2 * C::kTileBytes);
-                tma_tile<D>(C::kOwn, smem, &maps.k, hk, s.k0 + c0, &bars.own_full);
-                tma_tile<D>(C::kOwn + C::kTileBytes, smem, &maps.v, hk, s.k0 + c0, &bars.own_full);
-            }
-            bool ok = true;
-            int put = 0;
-            for (int it = 0; it < total; ++it) {
-                const int st = it % C::kStages, h = hk * group + it / per_head, r0 = (start + it % per_head) * kTile;
-                // -lse in log2 units, -inf (weight zero) where there is no query or it sees nothing; -delta
-                float ls[4], de[4];
+        if (lane == 0 && total > 0) {
+            tc::mbar_arrive_expect_tx(&bars.own_full, 2 * C::kTileBytes);
+            tma_tile<D>(C::kOwn, smem, &maps.k, hk, s.k0 + c0, &bars.own_full);
+            tma_tile<D>(C::kOwn + C::kTileBytes, smem, &maps.v, hk, s.k0 + c0, &bars.own_full);
+            load_ring<D>(bars, total, nullptr, [&](int k, uint32_t at, uint64_t *bar) {
+                tma_tile<D>(at, smem, k & 1 ? &maps.g : &maps.q, head_of(k >> 1), s.q0 + row_of(k >> 1), bar);
+            });
+        }
+    } else if (warp == 19) {
+        // -lse in log2 units, -inf (weight zero) where there is no query or it sees nothing; -delta.  Read a
+        // turn before they are needed: the loads wait long behind the tiles' traffic.
+        const int64_t at0 = stat_at(a.bt, s.q0, 0);   // a head's rows of a sequence lie side by side
+        float ls[4], de[4];
+        int h = hk * group, r0 = start * kTile;
+        auto fetch = [&]() {
+            const int64_t at = at0 + (int64_t)h * a.bt.Tq + r0 + lane;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = r0 + e * 32 + lane;
-                    ls[e] = -CUDART_INF_F;
-                    de[e] = 0.f;
-                    if (r < s.nq) {
-                        const int64_t at = stat_at(a.bt, s.q0 + r, h);
-                        const float x = a.lse[at] * kLog2e;
-                        ls[e] = x == -CUDART_INF_F ? x : -x;
-                        de[e] = -a.delta[at];
-                    }
-                }
-                if (it >= C::kStages) ok = warp_wait(&bars.empty[st], (it / C::kStages - 1) & 1, abort);
-                if (!ok) break;
-                if (lane == 0) {
-                    const uint32_t at = C::kRing + st * 2 * C::kTileBytes;
-                    tc::mbar_arrive_expect_tx(&bars.full[st], 2 * C::kTileBytes);
-                    tma_tile<D>(at, smem, &maps.q, h, s.q0 + r0, &bars.full[st]);
-                    tma_tile<D>(at + C::kTileBytes, smem, &maps.g, h, s.q0 + r0, &bars.full[st]);
-                }
-                ++put;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    stats[st * 2 * kTile + e * 32 + lane] = ls[e];
-                    stats[st * 2 * kTile + kTile + e * 32 + lane] = de[e];
-                }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars.stats[st]);
+            for (int e = 0; e < 4; ++e) {
+                const bool there = r0 + e * 32 + lane < s.nq;
+                ls[e] = there ? __ldg(a.lse + at + e * 32) : -CUDART_INF_F;
+                de[e] = there ? __ldg(a.delta + at + e * 32) : 0.f;
             }
-            if (!ok && lane == 0) drain_loads<D>(bars, put);
+            if ((r0 += kTile) >= s.nq) r0 = start * kTile, ++h;
+        };
+        if (total > 0) fetch();
+        for (int it = 0; it < total; ++it) {
+            float l[4], d[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                l[e] = ls[e] == -CUDART_INF_F ? ls[e] : -ls[e] * kLog2e;
+                d[e] = -de[e];
+            }
+            if (it + 1 < total) fetch();
+            if (it >= 2 && !warp_wait(&bars.stats_read[it & 1], (it / 2 - 1) & 1, abort)) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                stats[(it & 1) * 2 * kTile + e * 32 + lane] = l[e];
+                stats[(it & 1) * 2 * kTile + kTile + e * 32 + lane] = d[e];
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars.stats[it & 1]);
         }
     } else if (warp == 18) {
-        // queries that are not there are summed over with weight zero
-        watch_loads<D>(bars, smem + C::kRing, total, 2, lane,
-                       [&](int k) { return s.nq - (start + k % per_head) * kTile; });
+        // Queries that are not there are summed over with weight zero.  The word on the next Q goes with the
+        // weights of this turn, that on the next dO with its dS; each word belongs to one turn.
+        bool ok = total > 0;
+        for (int it = 0; it <= total && ok; ++it) {
+            const int left = it < total ? s.nq - row_of(it) : kTile;
+            for (int x = 0; x < 2 && ok; ++x) {
+                if (it < total && !(ok = watch_load<D>(bars, smem, 2 * it + x, left, lane))) break;
+                if (it == 0) {
+                    if (x == 1 && lane == 0) tc::mbar_arrive(&bars.first);
+                    continue;
+                }
+                uint64_t *word = x ? &bars.b_ready : &bars.a_ready;
+                if (lane == 0) tc::mbar_arrive(word);
+                if (x == 1) ok = warp_wait(&bars.b_ready, (it - 1) & 1, abort);   // a_ready's turn is over, too
+            }
+        }
     } else if (warp == 16) {
         constexpr uint32_t idS = tc::make_idesc_bf16(kTile, kTile, false, false);
         constexpr uint32_t idG = tc::make_idesc_bf16(kTile, D, false, true);
@@ -256,31 +287,30 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
         if (total > 0) {
             ok = warp_wait(&bars.own_full, 0, abort) && warp_wait(&bars.first, 0, abort);
             if (ok) {
-                chain_ss<D>(tS, desc_k(sK, 0), desc_k(sbase + C::kRing, 0), idS, leader);
+                chain_ss<D>(tS, desc_k(sK, 0), desc_k(sbase + stage_of<D>(0), 0), idS, leader);
                 commit_by(&bars.s_full, leader);
-                chain_ss<D>(tP, desc_k(sV, 0), desc_k(sbase + C::kRing + C::kTileBytes, 0), idS, leader);
+                chain_ss<D>(tP, desc_k(sV, 0), desc_k(sbase + stage_of<D>(1), 0), idS, leader);
                 commit_by(&bars.dp_full[0], leader);
             }
         }
         for (int it = 0; it < total && ok; ++it) {
-            const uint32_t q = sbase + C::kRing + (it % C::kStages) * 2 * C::kTileBytes, g = q + C::kTileBytes;
-            const uint32_t qn = sbase + C::kRing + ((it + 1) % C::kStages) * 2 * C::kTileBytes;
             const bool more = it + 1 < total;
             if (!(ok = warp_wait(&bars.a_ready, it & 1, abort))) break;
             tc::tc_fence_after();
-            chain_ts32(tV, tS, desc_mn(g, 0), idG, it > 0, leader);
+            chain_ts32(tV, tS, desc_mn(sbase + stage_of<D>(2 * it + 1), 0), idG, it > 0, leader);
             if (more) {
-                chain_ss<D>(tS, desc_k(sK, 0), desc_k(qn, 0), idS, leader);
+                chain_ss<D>(tS, desc_k(sK, 0), desc_k(sbase + stage_of<D>(2 * it + 2), 0), idS, leader);
                 commit_by(&bars.s_full, leader);
             }
+            commit_by(&bars.empty[(2 * it + 1) % C::kStages], leader);
             if (!(ok = warp_wait(&bars.b_ready, it & 1, abort))) break;
             tc::tc_fence_after();
-            chain_ts32(tK, tP, desc_mn(q, 0), idG, it > 0, leader);
+            chain_ts32(tK, tP, desc_mn(sbase + stage_of<D>(2 * it), 0), idG, it > 0, leader);
             if (more) {
-                chain_ss<D>(tP, desc_k(sV, 0), desc_k(qn + C::kTileBytes, 0), idS, leader);
+                chain_ss<D>(tP, desc_k(sV, 0), desc_k(sbase + stage_of<D>(2 * it + 3), 0), idS, leader);
                 commit_by(&bars.dp_full[0], leader);
             }
-            commit_by(more ? &bars.empty[it % C::kStages] : &bars.done, leader);
+            commit_by(more ? &bars.empty[(2 * it) % C::kStages] : &bars.done, leader);
         }
         if (!ok) {   // no product in flight when the memory is given back
             int quit = 0;
@@ -294,12 +324,12 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
         const float2 sc2 = make_float2(sc, sc);
         bool ok = true;
         for (int it = 0; it < total; ++it) {
-            const int st = it % C::kStages, r0 = (start + it % per_head) * kTile + part * 32;
-            const float *ls = stats + st * 2 * kTile + part * 32, *de = ls + kTile;
+            const int r0 = row_of(it) + part * 32;
+            const float *ls = stats + (it & 1) * 2 * kTile + part * 32, *de = ls + kTile;
             // this row's key is seen by the tile's queries from column `from` on
             const int from = c0 + row - ahead - r0;
             const bool partly = a.causal && c0 + (warp & 3) * 32 + 31 - ahead - r0 > 0;
-            ok = warp_wait(&bars.stats[st], (it / C::kStages) & 1, abort) && warp_wait(&bars.s_full, it & 1, abort);
+            ok = warp_wait(&bars.stats[it & 1], (it >> 1) & 1, abort) && warp_wait(&bars.s_full, it & 1, abort);
             if (!ok) break;
             tc::tc_fence_after();
             float2 p[16];
@@ -348,6 +378,7 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
             }
             put_operand(tP + lanes, p);
             arrive_operand(&bars.b_ready, lane);
+            if (lane == 0) tc::mbar_arrive(&bars.stats_read[it & 1]);
         }
         if (ok && total > 0) ok = warp_wait(&bars.done, 0, abort);
         if (ok && part < 2) {
@@ -387,64 +418,60 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
     const int h = blockIdx.x % a.bt.Hq, hk = h / (a.bt.Hq / a.bt.Hkv), r0 = t * kTile;
     const int total = (keys_seen(s, min(r0 + kTile, s.nq) - 1, a.causal) + kTile - 1) / kTile;
 
-    const uint32_t tmem = grad_setup<D>(bars);
+    const uint32_t tmem = grad_setup<D>(bars, 16);
     volatile int *abort = &bars.abort;
     const uint32_t tS = tmem, tP = tmem + kTile, tQ = tmem + 3 * kTile;
 
+    // turn j is key tile j: K is load 2 j, V load 2 j + 1
     if (warp == 17) {
         if (lane == 0) {
-            tc::mbar_arrive_expect_tx(&bars.own_full, 3 * C::kTileBytes);
+            tc::mbar_arrive_expect_tx(&bars.own_full, 2 * C::kTileBytes);
             tma_tile<D>(C::kOwn, smem, &maps.q, h, s.q0 + r0, &bars.own_full);
             tma_tile<D>(C::kOwn + C::kTileBytes, smem, &maps.g, h, s.q0 + r0, &bars.own_full);
-            tma_tile<D>(C::kOut, smem, &maps.o, h, s.q0 + r0, &bars.own_full);
-            bool ok = true;
-            int put = 0;
-            for (int j = 0; j < total; ++j) {
-                const int st = j % C::kStages;
-                if (j >= C::kStages) ok = tc::mbar_wait(&bars.empty[st], (j / C::kStages - 1) & 1, abort);
-                if (!ok) break;
-                const uint32_t at = C::kRing + st * 2 * C::kTileBytes;
-                tc::mbar_arrive_expect_tx(&bars.full[st], 2 * C::kTileBytes);
-                tma_tile<D>(at, smem, &maps.k, hk, s.k0 + (int64_t)j * kTile, &bars.full[st]);
-                tma_tile<D>(at + C::kTileBytes, smem, &maps.v, hk, s.k0 + (int64_t)j * kTile, &bars.full[st]);
-                ++put;
-            }
-            if (!ok) drain_loads<D>(bars, put);
+            tc::mbar_arrive_expect_tx(&bars.out_full, C::kTileBytes);
+            tma_tile<D>(C::kOut, smem, &maps.o, h, s.q0 + r0, &bars.out_full);
+            load_ring<D>(bars, total, &bars.out_read, [&](int k, uint32_t at, uint64_t *bar) {
+                tma_tile<D>(at, smem, k & 1 ? &maps.v : &maps.k, hk, s.k0 + (int64_t)(k >> 1) * kTile, bar);
+            });
         }
     } else if (warp == 18) {
-        // keys that are not there are summed over with weight zero (their values only masked)
-        watch_loads<D>(bars, smem + C::kRing, total, 1, lane, [&](int k) { return s.nk - k * kTile; });
+        // keys that are not there are summed over with weight zero (their values only masked); the word on
+        // the next K and V goes with the reading of this turn's scores
+        bool ok = total > 0;
+        for (int j = 0; j < total && ok; ++j) {
+            ok = watch_load<D>(bars, smem, 2 * j, s.nk - j * kTile, lane) && watch_load<D>(bars, smem, 2 * j + 1, kTile, lane);
+            if (!ok) break;
+            if (lane == 0) tc::mbar_arrive(j == 0 ? &bars.first : &bars.a_ready);
+            if (j > 0) ok = warp_wait(&bars.a_ready, (j - 1) & 1, abort);
+        }
     } else if (warp == 16) {
         constexpr uint32_t idS = tc::make_idesc_bf16(kTile, kTile, false, false);
         constexpr uint32_t idG = tc::make_idesc_bf16(kTile, D, false, true);
         const uint32_t leader = elect_lane();
         const uint32_t sQ = sbase + C::kOwn, sG = sQ + C::kTileBytes;
         bool ok = true;
+        auto scores = [&](int j) {
+            chain_ss<D>(tS, desc_k(sQ, 0), desc_k(sbase + stage_of<D>(2 * j), 0), idS, leader);
+            commit_by(&bars.s_full, leader);
+            chain_ss<D>(tP + (j & 1) * kTile, desc_k(sG, 0), desc_k(sbase + stage_of<D>(2 * j + 1), 0), idS, leader);
+            commit_by(&bars.dp_full[j & 1], leader);
+            commit_by(&bars.empty[(2 * j + 1) % C::kStages], leader);
+        };
         if (total > 0) {
             ok = warp_wait(&bars.own_full, 0, abort) && warp_wait(&bars.first, 0, abort);
-            if (ok) {
-                chain_ss<D>(tS, desc_k(sQ, 0), desc_k(sbase + C::kRing, 0), idS, leader);
-                commit_by(&bars.s_full, leader);
-                chain_ss<D>(tP, desc_k(sG, 0), desc_k(sbase + C::kRing + C::kTileBytes, 0), idS, leader);
-                commit_by(&bars.dp_full[0], leader);
-            }
+            if (ok) scores(0);
         }
         for (int j = 0; j < total && ok; ++j) {
-            const uint32_t k = sbase + C::kRing + (j % C::kStages) * 2 * C::kTileBytes;
-            const uint32_t kn = sbase + C::kRing + ((j + 1) % C::kStages) * 2 * C::kTileBytes;
             const bool more = j + 1 < total;
             if (more) {   // the next scores as soon as these have been read; dP alternates between two places
                 if (!(ok = warp_wait(&bars.a_ready, j & 1, abort))) break;
                 tc::tc_fence_after();
-                chain_ss<D>(tS, desc_k(sQ, 0), desc_k(kn, 0), idS, leader);
-                commit_by(&bars.s_full, leader);
-                chain_ss<D>(tP + ((j + 1) & 1) * kTile, desc_k(sG, 0), desc_k(kn + C::kTileBytes, 0), idS, leader);
-                commit_by(&bars.dp_full[(j + 1) & 1], leader);
+                scores(j + 1);
             }
             if (!(ok = warp_wait(&bars.b_ready, j & 1, abort))) break;
             tc::tc_fence_after();
-            chain_ts32(tQ, tP + (j & 1) * kTile, desc_mn(k, 0), idG, j > 0, leader);
-            commit_by(more ? &bars.empty[j % C::kStages] : &bars.done, leader);
+            chain_ts32(tQ, tP + (j & 1) * kTile, desc_mn(sbase + stage_of<D>(2 * j), 0), idG, j > 0, leader);
+            commit_by(more ? &bars.empty[(2 * j) % C::kStages] : &bars.done, leader);
         }
         if (!ok) {   // no product in flight when the memory is given back
             int quit = 0;
@@ -464,7 +491,7 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
             ls = a.lse[at] * kLog2e;
             if (ls != -CUDART_INF_F) ls = -ls;
         }
-        bool ok = warp_wait(&bars.own_full, 0, abort);
+        bool ok = warp_wait(&bars.own_full, 0, abort) && warp_wait(&bars.out_full, 0, abort);
         float de = 0.f;
         if (ok) {   // delta = dO . O of this row, the same in all four groups
             const uint8_t *g = smem + C::kOwn + C::kTileBytes, *o = smem + C::kOut;
@@ -480,6 +507,8 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                 }
             }
             if (part == 0 && r < s.nq) a.delta[at] = de;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars.out_read);
         }
         const float2 sc2 = make_float2(sc, sc), ls2 = make_float2(ls, ls), de2 = make_float2(-de, -de);
         for (int j = 0; j < total && ok; ++j) {
