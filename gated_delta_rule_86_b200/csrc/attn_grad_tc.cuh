@@ -30,10 +30,13 @@ namespace attn {
 
 template <int D> struct GradCfg {
     static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kStages = D == 128 ? 5 : 8;      // of one tile each, released one by one
+    // Stages of one tile each, released one by one: of a turn's two tiles (Q and dO, or K and V) the first
+    // is read again at the turn's end, so more of it are held.  (One ring for both: 262 us for dQ at B2
+    // T4096 H16, its loads of V waiting for dQ's products.)
+    static constexpr int kFirst = D == 128 ? 3 : 4, kSecond = D == 128 ? 2 : 4, kStages = kFirst + kSecond;
     static constexpr int kOwn = 0;                        // the block's own two tiles
     static constexpr int kRing = 2 * kTileBytes;
-    static constexpr int kOut = kRing + (kStages - 1) * kTileBytes;   // queries' kernel: O, in the last stage at first
+    static constexpr int kOut = kRing + (kFirst - 1) * kTileBytes;    // queries' kernel: O, in a stage filled late
     static constexpr int kStats = kRing + kStages * kTileBytes;       // keys' kernel: -lse and -delta of two turns' queries
     static constexpr int kBars = kStats + 2 * 2 * kTile * 4;
     static constexpr int kSmem = kBars + 512;
@@ -86,13 +89,21 @@ template <int D> __device__ __forceinline__ uint32_t grad_setup(GradBars &bars, 
     return bars.tmem;
 }
 
-// Load number k, counted from the first, lies in stage k mod kStages.
+// Load k is tile k & 1 of turn k >> 1: its stage, the parity of that stage's filling, and its place.
+template <int D> __device__ __forceinline__ int stage_no(int k) {
+    using C = GradCfg<D>;
+    return k & 1 ? C::kFirst + (k >> 1) % C::kSecond : (k >> 1) % C::kFirst;
+}
+template <int D> __device__ __forceinline__ uint32_t filling(int k) {
+    using C = GradCfg<D>;
+    return (k >> 1) / (k & 1 ? C::kSecond : C::kFirst);
+}
 template <int D> __device__ __forceinline__ uint32_t stage_of(int k) {
-    return GradCfg<D>::kRing + (k % GradCfg<D>::kStages) * GradCfg<D>::kTileBytes;
+    return GradCfg<D>::kRing + stage_no<D>(k) * GradCfg<D>::kTileBytes;
 }
 
-// Warp 17's lane: loads `total` pairs of tiles, pair(k, bar, at) issuing tile k & 1 of pair k >> 1.  The
-// last stage's first filling waits for `hold`, if given.
+// Warp 17's lane: loads both tiles of `total` turns, issue(k, place, barrier) starting load k.  The stage
+// that holds O at first waits for `hold`, if given.
 template <int D, typename F>
 __device__ __forceinline__ void load_ring(GradBars &bars, int total, uint64_t *hold, F issue) {
     using C = GradCfg<D>;
@@ -100,9 +111,10 @@ __device__ __forceinline__ void load_ring(GradBars &bars, int total, uint64_t *h
     bool ok = true;
     int k = 0;
     for (; k < 2 * total; ++k) {
-        const int st = k % C::kStages;
-        if (k >= C::kStages) ok = tc::mbar_wait(&bars.empty[st], (k / C::kStages - 1) & 1, abort);
-        else if (hold && k == C::kStages - 1) ok = tc::mbar_wait(hold, 0, abort);
+        const int st = stage_no<D>(k);
+        const uint32_t n = filling<D>(k);
+        if (n > 0) ok = tc::mbar_wait(&bars.empty[st], (n - 1) & 1, abort);
+        else if (hold && stage_of<D>(k) == C::kOut) ok = tc::mbar_wait(hold, 0, abort);
         if (!ok) break;
         tc::mbar_arrive_expect_tx(&bars.full[st], C::kTileBytes);
         issue(k, stage_of<D>(k), &bars.full[st]);
@@ -110,17 +122,16 @@ __device__ __forceinline__ void load_ring(GradBars &bars, int total, uint64_t *h
     if (!ok) {   // a wait ran out: leave no copy in flight
         int quit = 0;
         tc::mbar_wait(&bars.own_full, 0, &quit);
-        for (int i = k > C::kStages ? k - C::kStages : 0; i < k; ++i) {
+        for (int i = k > 2 * C::kFirst ? k - 2 * C::kFirst : 0; i < k; ++i) {
             quit = 0;
-            tc::mbar_wait(&bars.full[i % C::kStages], (i / C::kStages) & 1, &quit);
+            tc::mbar_wait(&bars.full[stage_no<D>(i)], filling<D>(i) & 1, &quit);
         }
     }
 }
 
 // Warp 18: waits for load k and zeroes its rows from `rows` on, where that is below 128.
 template <int D> __device__ __forceinline__ bool watch_load(GradBars &bars, uint8_t *smem, int k, int rows, int lane) {
-    using C = GradCfg<D>;
-    if (!warp_wait(&bars.full[k % C::kStages], (k / C::kStages) & 1, &bars.abort)) return false;
+    if (!warp_wait(&bars.full[stage_no<D>(k)], filling<D>(k) & 1, &bars.abort)) return false;
     if (rows < kTile) {
         zero_rows<D>(smem + stage_of<D>(k), rows, lane);
         __syncwarp();
@@ -302,7 +313,7 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
                 chain_ss<D>(tS, desc_k(sK, 0), desc_k(sbase + stage_of<D>(2 * it + 2), 0), idS, leader);
                 commit_by(&bars.s_full, leader);
             }
-            commit_by(&bars.empty[(2 * it + 1) % C::kStages], leader);
+            commit_by(&bars.empty[stage_no<D>(2 * it + 1)], leader);
             if (!(ok = warp_wait(&bars.b_ready, it & 1, abort))) break;
             tc::tc_fence_after();
             chain_ts32(tK, tP, desc_mn(sbase + stage_of<D>(2 * it), 0), idG, it > 0, leader);
@@ -310,7 +321,7 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
                 chain_ss<D>(tP, desc_k(sV, 0), desc_k(sbase + stage_of<D>(2 * it + 3), 0), idS, leader);
                 commit_by(&bars.dp_full[0], leader);
             }
-            commit_by(more ? &bars.empty[(2 * it) % C::kStages] : &bars.done, leader);
+            commit_by(more ? &bars.empty[stage_no<D>(2 * it)] : &bars.done, leader);
         }
         if (!ok) {   // no product in flight when the memory is given back
             int quit = 0;
@@ -455,7 +466,7 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
             commit_by(&bars.s_full, leader);
             chain_ss<D>(tP + (j & 1) * kTile, desc_k(sG, 0), desc_k(sbase + stage_of<D>(2 * j + 1), 0), idS, leader);
             commit_by(&bars.dp_full[j & 1], leader);
-            commit_by(&bars.empty[(2 * j + 1) % C::kStages], leader);
+            commit_by(&bars.empty[stage_no<D>(2 * j + 1)], leader);
         };
         if (total > 0) {
             ok = warp_wait(&bars.own_full, 0, abort) && warp_wait(&bars.first, 0, abort);
@@ -471,7 +482,7 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
             if (!(ok = warp_wait(&bars.b_ready, j & 1, abort))) break;
             tc::tc_fence_after();
             chain_ts32(tQ, tP + (j & 1) * kTile, desc_mn(sbase + stage_of<D>(2 * j), 0), idG, j > 0, leader);
-            commit_by(more ? &bars.empty[(2 * j) % C::kStages] : &bars.done, leader);
+            commit_by(more ? &bars.empty[stage_no<D>(2 * j)] : &bars.done, leader);
         }
         if (!ok) {   // no product in flight when the memory is given back
             int quit = 0;
