@@ -238,9 +238,11 @@ kda_status kda_attn_fwd(const void *q, const void *k, const void *v, int64_t q_s
     if (s != KDA_OK) return s;
     a.out = out;
     a.lse = lse;
+    if (Tq == 0) return KDA_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == KDA_F32)
-        return status_of(d == 64 ? launch_prompt<float, 64>(a, st) : launch_prompt<float, 128>(a, st));
+    const int sms = kda::device_sm_count();
+    if (sms < 1) return KDA_ERR_CUDA;
+    if (dtype == KDA_F32) return status_of(d == 64 ? launch_prompt<64>(a, sms, st) : launch_prompt<128>(a, sms, st));
     return status_of(d == 64 ? launch_prompt_tc<64>(a, st) : launch_prompt_tc<128>(a, st));
 }
 
@@ -274,8 +276,10 @@ kda_status kda_attn_bwd(const void *q, const void *k, const void *v, int64_t q_s
     a.dk = dk;
     a.dv = dv;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int sms = kda::device_sm_count();
+    if (sms < 1) return KDA_ERR_CUDA;
     if (dtype == KDA_F32)
-        return status_of(d == 64 ? launch_prompt_grad<float, 64>(a, st) : launch_prompt_grad<float, 128>(a, st));
+        return status_of(d == 64 ? launch_prompt_grad<64>(a, sms, st) : launch_prompt_grad<128>(a, sms, st));
     return status_of(d == 64 ? launch_prompt_grad_tc<64>(a, st) : launch_prompt_grad_tc<128>(a, st));
 }
 

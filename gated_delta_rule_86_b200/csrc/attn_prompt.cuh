@@ -12,9 +12,10 @@
 // seven products in place of five.)
 //
 // fp32 inputs ask for fp32 accuracy, which the tensor cores' operands do not give; these kernels are
-// bound by the FMA units.  Tiles of 64 x 64 scores; thread (ty, tx) of 16 x 16 holds rows
+// bound by the FMA units and, for small batches, by the latency of a tile.  A block has ROWS rows of one
+// head and walks tiles of 64 of the other side; thread (ty, tx) holds 4 x 4 scores, rows
 // 4 ty .. 4 ty + 3, so a row's 16 threads lie in one half of a warp and its maximum and sum are four
-// shuffles.
+// shuffles.  The next tile is on its way (cp.async) while one is worked on.
 #pragma once
 
 #include "attn_append.cuh"
@@ -43,25 +44,34 @@ __device__ __forceinline__ int64_t stat_at(const Batch &bt, int64_t row, int h) 
     return (b * bt.Hq + h) * bt.Tq + (row - b * bt.Tq);
 }
 
-constexpr int kPT = 64;         // queries and keys of a tile
-constexpr int kPThreads = 256;
+constexpr int kPT = 64;   // rows of a tile of the other side
 
-// Rows [r0, r0 + 64) of a token tensor's head into shared memory as fp32, row pitch D + 4; rows at or
-// past `rows` are zero.
-template <typename T, int D>
-__device__ __forceinline__ void stage_rows(float *dst, const T *src, int64_t stride, int r0, int rows, float mul) {
-    constexpr int VE = Vec16<T>::N;
-    for (int i = threadIdx.x; i < kPT * D / VE; i += kPThreads) {
-        const int r = i / (D / VE), c = i % (D / VE) * VE;
-        float *d = dst + r * (D + 4) + c;
-        if (r0 + r < rows) {
-            const Vec16<T> x = load16(src + (int64_t)(r0 + r) * stride + c);
-#pragma unroll
-            for (int e = 0; e < VE; ++e) d[e] = to_f32(x.x[e]) * mul;
-        } else {
-#pragma unroll
-            for (int e = 0; e < VE; ++e) d[e] = 0.f;
-        }
+template <int D> struct PromptCfg {
+    static constexpr int kPitch = D + 4;           // floats of a staged row
+    static constexpr int kTileF = kPT * kPitch;
+    // own tiles of `rows` rows, two tiles of the other side twice, weights [rows][68], statistics
+    static constexpr int smem(int rows, int own) {
+        return (own * rows * kPitch + 4 * kTileF + rows * 68 + 2 * 2 * kPT) * 4 + 160;
+    }
+};
+
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// Rows [r0, r0 + N) of a head into shared memory, zeros at or past `rows`.
+template <int D, int N, int THREADS>
+__device__ __forceinline__ void stage_rows(float *dst, const float *src, int64_t stride, int r0, int rows) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < N * D / 4; i += THREADS) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4;
+        const bool there = r0 + r < rows;
+        copy16(dst + r * (D + 4) + c, src + (there ? (int64_t)(r0 + r) * stride + c : 0), there);
     }
 }
 
@@ -83,7 +93,7 @@ template <int D> __device__ __forceinline__ void dot_rows(float (&acc)[4][4], co
     }
 }
 
-// acc[i][c] += sum_t W[4 ty + i][t] X[t][tx * D / 16 + c]  (W pitch 68, X pitch D + 4)
+// acc[i][c] += sum_t W[4 ty + i][t] X[t][channel c of tx]  (W pitch 68, X pitch D + 4)
 template <int D> __device__ __forceinline__ void weigh_rows(float (&acc)[4][D / 16], const float *W, const float *X,
                                                             int ty, int tx) {
 #pragma unroll 2
@@ -109,37 +119,50 @@ template <int D> __device__ __forceinline__ void weigh_rows(float (&acc)[4][D / 
     }
 }
 
-// Channel of a thread's c-th accumulator in weigh_rows.
-__device__ __forceinline__ int weigh_channel(int tx, int c) { return tx * 4 + (c / 4) * 64 + c % 4; }
-
-template <typename T, int D>
-__device__ __forceinline__ void write_row(T *dst, const float (&acc)[D / 16], int tx, float mul) {
+// A thread's channels of one row: tx * 4 + {0 .. 3}, + 64 for the second four.
+template <int D> __device__ __forceinline__ void write_row(float *dst, const float (&acc)[D / 16], int tx, float mul) {
 #pragma unroll
-    for (int c = 0; c < D / 16; c += 4) {
-        T *p = dst + weigh_channel(tx, c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = from_f32<T>(acc[c + e] * mul);
-    }
+    for (int c = 0; c < D / 16; c += 4)
+        *reinterpret_cast<float4 *>(dst + tx * 4 + (c / 4) * 64) =
+            make_float4(acc[c] * mul, acc[c + 1] * mul, acc[c + 2] * mul, acc[c + 3] * mul);
 }
 
-template <int D> constexpr int prompt_smem(int tiles, int squares) {
-    return (tiles * kPT * (D + 4) + squares * kPT * 68) * 4 + 160;
+// A thread's 4 x 4 weights into shared memory; a row's come from the half warp that reads them.
+__device__ __forceinline__ void put_weights(float *sp, const float (&x)[4][4], int ty, int tx) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sp[(4 * ty + i) * 68 + tx + 16 * j] = x[i][j];
+    __syncwarp();
 }
 
-template <typename T, int D> __global__ void __launch_bounds__(kPThreads, 1) attn_prompt_kernel(const PromptArgs a) {
+template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_prompt_kernel(const PromptArgs a) {
+    using C = PromptCfg<D>;
+    constexpr int THREADS = ROWS * 4;
     extern __shared__ __align__(16) float sm[];
-    float *sq = sm, *sk = sq + kPT * (D + 4), *sv = sk + kPT * (D + 4), *sp = sv + kPT * (D + 4);
-    int *scratch = reinterpret_cast<int *>(sp + kPT * 68);
+    float *sq = sm, *ring = sq + ROWS * C::kPitch, *sp = ring + 4 * C::kTileF;
+    int *scratch = reinterpret_cast<int *>(sp + ROWS * 68 + 4 * kPT);
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, h = blockIdx.y;
     int n, t;
-    if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, kPT, blockIdx.x, scratch, n, t)) return;
+    if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, ROWS, gridDim.x - 1 - blockIdx.x, scratch, n, t)) return;
     const Seq s = seq_of(a.bt, n);
-    const int r0 = t * kPT, hk = h / (a.bt.Hq / a.bt.Hkv);
-    const T *q = static_cast<const T *>(a.q) + s.q0 * a.q_stride + (int64_t)h * D;
-    const T *k = static_cast<const T *>(a.k) + s.k0 * a.k_stride + (int64_t)hk * D;
-    const T *v = static_cast<const T *>(a.v) + s.k0 * a.v_stride + (int64_t)hk * D;
-    stage_rows<T, D>(sq, q, a.q_stride, r0, s.nq, a.scale * kLog2e);
+    const int r0 = t * ROWS, hk = h / (a.bt.Hq / a.bt.Hkv);
+    const float *q = static_cast<const float *>(a.q) + s.q0 * a.q_stride + (int64_t)h * D;
+    const float *k = static_cast<const float *>(a.k) + s.k0 * a.k_stride + (int64_t)hk * D;
+    const float *v = static_cast<const float *>(a.v) + s.k0 * a.v_stride + (int64_t)hk * D;
+    const int end = keys_seen(s, min(r0 + ROWS, s.nq) - 1, a.causal);
+    auto load = [&](int c0, int into) {
+        if (c0 < end) {
+            stage_rows<D, kPT, THREADS>(ring + 2 * into * C::kTileF, k, a.k_stride, c0, s.nk);
+            stage_rows<D, kPT, THREADS>(ring + (2 * into + 1) * C::kTileF, v, a.v_stride, c0, s.nk);
+        }
+        copies_commit();
+    };
+    stage_rows<D, ROWS, THREADS>(sq, q, a.q_stride, r0, s.nq);
+    load(0, 0);
 
+    const float sc = a.scale * kLog2e;
     float m[4], l[4], o[4][D / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -148,21 +171,20 @@ template <typename T, int D> __global__ void __launch_bounds__(kPThreads, 1) att
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
     }
-    const int end = keys_seen(s, min(r0 + kPT, s.nq) - 1, a.causal);
-    for (int c0 = 0; c0 < end; c0 += kPT) {
+    int at = 0;
+    for (int c0 = 0; c0 < end; c0 += kPT, at ^= 1) {
+        copies_wait();
         __syncthreads();
-        stage_rows<T, D>(sk, k, a.k_stride, c0, s.nk, 1.f);
-        stage_rows<T, D>(sv, v, a.v_stride, c0, s.nk, 1.f);
-        __syncthreads();
+        load(c0 + kPT, at ^ 1);
         float x[4][4] = {};
-        dot_rows<D>(x, sq, sk, ty, tx);
+        dot_rows<D>(x, sq, ring + 2 * at * C::kTileF, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int seen = keys_seen(s, r0 + 4 * ty + i, a.causal) - c0;
             float top = -CUDART_INF_F;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (tx + 16 * j >= seen) x[i][j] = -CUDART_INF_F;
+                x[i][j] = tx + 16 * j < seen ? x[i][j] * sc : -CUDART_INF_F;
                 top = fmaxf(top, x[i][j]);
             }
 #pragma unroll
@@ -173,16 +195,16 @@ template <typename T, int D> __global__ void __launch_bounds__(kPThreads, 1) att
             l[i] *= f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float p = exp2f(x[i][j] - base);
-                l[i] += p;
-                sp[(4 * ty + i) * 68 + tx + 16 * j] = p;
+                x[i][j] = exp2f(x[i][j] - base);
+                l[i] += x[i][j];
             }
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
         }
-        __syncwarp();   // a row's weights come from the half warp that reads them
-        weigh_rows<D>(o, sp, sv, ty, tx);
+        put_weights(sp, x, ty, tx);
+        weigh_rows<D>(o, sp, ring + (2 * at + 1) * C::kTileF, ty, tx);
     }
+    copies_wait();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + 4 * ty + i;
@@ -191,7 +213,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kPThreads, 1) att
         for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (r >= s.nq) continue;
         const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-        write_row<T, D>(static_cast<T *>(a.out) + ((s.q0 + r) * a.bt.Hq + h) * D, o[i], tx, inv);
+        write_row<D>(static_cast<float *>(a.out) + ((s.q0 + r) * a.bt.Hq + h) * D, o[i], tx, inv);
         if (a.lse && tx == 0)
             a.lse[stat_at(a.bt, s.q0 + r, h)] =
                 sum == 0.f ? -CUDART_INF_F : m[i] * 0.69314718055994531f + logf(sum);
@@ -200,7 +222,8 @@ template <typename T, int D> __global__ void __launch_bounds__(kPThreads, 1) att
 
 // delta_i = dO_i . O_i, one warp per (query, head).  Rows behind the last sequence get zero gradients
 // here: no other kernel visits them.
-template <typename T, int D> __global__ void __launch_bounds__(256) attn_delta_kernel(const PromptArgs a) {
+template <int D> __global__ void __launch_bounds__(256) attn_delta_kernel(const PromptArgs a) {
+    using T = float;
     constexpr int VE = Vec16<T>::N;
     constexpr int LANES = D / VE;   // lanes of a row
     const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
@@ -246,10 +269,11 @@ __device__ __forceinline__ void grad_scores(float (&x)[4][4], float (&y)[4][4], 
         }
 }
 
-// lse (in log2 units; 0 for rows that see nothing) and delta of 64 queries
+// lse (in log2 units; 0 for rows that see nothing) and delta of N queries
+template <int N, int THREADS>
 __device__ __forceinline__ void stage_stats(float *lse2, float *delta, const PromptArgs &a, const Seq &s, int r0, int h) {
-    if (threadIdx.x < kPT) {
-        const int r = r0 + threadIdx.x;
+    for (int i = threadIdx.x; i < N; i += THREADS) {
+        const int r = r0 + i;
         float x = 0.f, y = 0.f;
         if (r < s.nq) {
             const int64_t at = stat_at(a.bt, s.q0 + r, h);
@@ -257,113 +281,130 @@ __device__ __forceinline__ void stage_stats(float *lse2, float *delta, const Pro
             y = a.delta[at];
             if (x == -CUDART_INF_F) x = 0.f;
         }
-        lse2[threadIdx.x] = x;
-        delta[threadIdx.x] = y;
+        lse2[i] = x;
+        delta[i] = y;
     }
 }
 
-// dK and dV of 64 keys of one head of the cache, over all query heads of its group.
-template <typename T, int D> __global__ void __launch_bounds__(kPThreads, 1) attn_grad_kv_kernel(const PromptArgs a) {
+// dK and dV of ROWS keys of one head of the cache, over all query heads of its group.
+template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_grad_kv_kernel(const PromptArgs a) {
+    using C = PromptCfg<D>;
+    constexpr int THREADS = ROWS * 4;
     extern __shared__ __align__(16) float sm[];
-    float *sk = sm, *sv = sk + kPT * (D + 4), *sq = sv + kPT * (D + 4), *sg = sq + kPT * (D + 4),
-          *sp = sg + kPT * (D + 4);
-    __shared__ float lse2[kPT], delta[kPT];
-    int *scratch = reinterpret_cast<int *>(sp + kPT * 68);
+    float *sk = sm, *sv = sk + ROWS * C::kPitch, *ring = sv + ROWS * C::kPitch, *sp = ring + 4 * C::kTileF,
+          *stats = sp + ROWS * 68;   // lse and delta of two tiles
+    int *scratch = reinterpret_cast<int *>(stats + 4 * kPT);
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, hk = blockIdx.y;
     int n, t;
-    if (!find_tile(a.bt.cu_k, a.bt.n, a.bt.Tk, kPT, blockIdx.x, scratch, n, t)) return;
+    if (!find_tile(a.bt.cu_k, a.bt.n, a.bt.Tk, ROWS, blockIdx.x, scratch, n, t)) return;
     const Seq s = seq_of(a.bt, n);
-    const int c0 = t * kPT, group = a.bt.Hq / a.bt.Hkv;
-    stage_rows<T, D>(sk, static_cast<const T *>(a.k) + s.k0 * a.k_stride + (int64_t)hk * D, a.k_stride, c0, s.nk, 1.f);
-    stage_rows<T, D>(sv, static_cast<const T *>(a.v) + s.k0 * a.v_stride + (int64_t)hk * D, a.v_stride, c0, s.nk, 1.f);
-    float gk[4][D / 16] = {}, gv[4][D / 16] = {};
-    // the first query that sees key c0
-    const int start = a.causal ? max(0, c0 - (s.nk - s.nq)) / kPT * kPT : 0;
-    for (int h = hk * group; h < (hk + 1) * group; ++h) {
-        const T *q = static_cast<const T *>(a.q) + s.q0 * a.q_stride + (int64_t)h * D;
-        const T *g = static_cast<const T *>(a.d_out) + (s.q0 * a.bt.Hq + h) * (int64_t)D;
-        for (int r0 = start; r0 < s.nq; r0 += kPT) {
-            __syncthreads();
-            stage_rows<T, D>(sq, q, a.q_stride, r0, s.nq, 1.f);
-            stage_rows<T, D>(sg, g, (int64_t)a.bt.Hq * D, r0, s.nq, 1.f);
-            stage_stats(lse2, delta, a, s, r0, h);
-            __syncthreads();
-            float x[4][4] = {}, y[4][4] = {};
-            dot_rows<D>(x, sk, sq, ty, tx);
-            dot_rows<D>(y, sv, sg, ty, tx);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[i][j] *= a.scale * kLog2e;
-            grad_scores(x, y, s, lse2, delta, r0, c0, ty, tx, a.causal, true);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sp[(4 * ty + i) * 68 + tx + 16 * j] = x[i][j];
-            __syncwarp();
-            weigh_rows<D>(gv, sp, sg, ty, tx);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sp[(4 * ty + i) * 68 + tx + 16 * j] = y[i][j];
-            __syncwarp();
-            weigh_rows<D>(gk, sp, sq, ty, tx);
+    const int c0 = t * ROWS, group = a.bt.Hq / a.bt.Hkv;
+    // the first tile of queries that sees key c0
+    const int start = a.causal ? max(0, c0 - (s.nk - s.nq)) / kPT : 0;
+    const int per_head = max(0, (s.nq + kPT - 1) / kPT - start), total = per_head * group;
+    auto load = [&](int it, int into) {
+        if (it < total) {
+            const int h = hk * group + it / per_head, r0 = (start + it % per_head) * kPT;
+            stage_rows<D, kPT, THREADS>(ring + 2 * into * C::kTileF,
+                                        static_cast<const float *>(a.q) + s.q0 * a.q_stride + (int64_t)h * D, a.q_stride,
+                                        r0, s.nq);
+            stage_rows<D, kPT, THREADS>(ring + (2 * into + 1) * C::kTileF,
+                                        static_cast<const float *>(a.d_out) + (s.q0 * a.bt.Hq + h) * (int64_t)D,
+                                        (int64_t)a.bt.Hq * D, r0, s.nq);
+            stage_stats<kPT, THREADS>(stats + 2 * into * kPT, stats + (2 * into + 1) * kPT, a, s, r0, h);
         }
+        copies_commit();
+    };
+    stage_rows<D, ROWS, THREADS>(sk, static_cast<const float *>(a.k) + s.k0 * a.k_stride + (int64_t)hk * D, a.k_stride, c0,
+                                 s.nk);
+    stage_rows<D, ROWS, THREADS>(sv, static_cast<const float *>(a.v) + s.k0 * a.v_stride + (int64_t)hk * D, a.v_stride, c0,
+                                 s.nk);
+    load(0, 0);
+    const float sc = a.scale * kLog2e;
+    float gk[4][D / 16] = {}, gv[4][D / 16] = {};
+    for (int it = 0; it < total; ++it) {
+        const int at = it & 1, r0 = (start + it % per_head) * kPT;
+        const float *sq = ring + 2 * at * C::kTileF, *sg = sq + C::kTileF;
+        copies_wait();
+        __syncthreads();
+        load(it + 1, at ^ 1);
+        float x[4][4] = {}, y[4][4] = {};
+        dot_rows<D>(x, sk, sq, ty, tx);
+        dot_rows<D>(y, sv, sg, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[i][j] *= sc;
+        grad_scores(x, y, s, stats + 2 * at * kPT, stats + (2 * at + 1) * kPT, r0, c0, ty, tx, a.causal, true);
+        put_weights(sp, x, ty, tx);
+        weigh_rows<D>(gv, sp, sg, ty, tx);
+        put_weights(sp, y, ty, tx);
+        weigh_rows<D>(gk, sp, sq, ty, tx);
     }
+    copies_wait();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = c0 + 4 * ty + i;
         if (r >= s.nk) continue;
-        const int64_t at = ((s.k0 + r) * a.bt.Hkv + hk) * D;
-        write_row<T, D>(static_cast<T *>(a.dk) + at, gk[i], tx, a.scale);
-        write_row<T, D>(static_cast<T *>(a.dv) + at, gv[i], tx, 1.f);
+        const int64_t to = ((s.k0 + r) * a.bt.Hkv + hk) * D;
+        write_row<D>(static_cast<float *>(a.dk) + to, gk[i], tx, a.scale);
+        write_row<D>(static_cast<float *>(a.dv) + to, gv[i], tx, 1.f);
     }
 }
 
-// dQ of 64 queries of one head.
-template <typename T, int D> __global__ void __launch_bounds__(kPThreads, 1) attn_grad_q_kernel(const PromptArgs a) {
+// dQ of ROWS queries of one head.
+template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_grad_q_kernel(const PromptArgs a) {
+    using C = PromptCfg<D>;
+    constexpr int THREADS = ROWS * 4;
     extern __shared__ __align__(16) float sm[];
-    float *sk = sm, *sv = sk + kPT * (D + 4), *sq = sv + kPT * (D + 4), *sg = sq + kPT * (D + 4),
-          *sp = sg + kPT * (D + 4);
-    __shared__ float lse2[kPT], delta[kPT];
-    int *scratch = reinterpret_cast<int *>(sp + kPT * 68);
+    float *sq = sm, *sg = sq + ROWS * C::kPitch, *ring = sg + ROWS * C::kPitch, *sp = ring + 4 * C::kTileF,
+          *stats = sp + ROWS * 68;
+    int *scratch = reinterpret_cast<int *>(stats + 4 * kPT);
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, h = blockIdx.y;
     int n, t;
-    if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, kPT, blockIdx.x, scratch, n, t)) return;
+    if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, ROWS, gridDim.x - 1 - blockIdx.x, scratch, n, t)) return;
     const Seq s = seq_of(a.bt, n);
-    const int r0 = t * kPT, hk = h / (a.bt.Hq / a.bt.Hkv);
-    const T *k = static_cast<const T *>(a.k) + s.k0 * a.k_stride + (int64_t)hk * D;
-    const T *v = static_cast<const T *>(a.v) + s.k0 * a.v_stride + (int64_t)hk * D;
-    stage_rows<T, D>(sq, static_cast<const T *>(a.q) + s.q0 * a.q_stride + (int64_t)h * D, a.q_stride, r0, s.nq,
-                     a.scale * kLog2e);
-    stage_rows<T, D>(sg, static_cast<const T *>(a.d_out) + (s.q0 * a.bt.Hq + h) * (int64_t)D, (int64_t)a.bt.Hq * D, r0,
-                     s.nq, 1.f);
-    stage_stats(lse2, delta, a, s, r0, h);
+    const int r0 = t * ROWS, hk = h / (a.bt.Hq / a.bt.Hkv);
+    const float *k = static_cast<const float *>(a.k) + s.k0 * a.k_stride + (int64_t)hk * D;
+    const float *v = static_cast<const float *>(a.v) + s.k0 * a.v_stride + (int64_t)hk * D;
+    const int end = keys_seen(s, min(r0 + ROWS, s.nq) - 1, a.causal);
+    auto load = [&](int c0, int into) {
+        if (c0 < end) {
+            stage_rows<D, kPT, THREADS>(ring + 2 * into * C::kTileF, k, a.k_stride, c0, s.nk);
+            stage_rows<D, kPT, THREADS>(ring + (2 * into + 1) * C::kTileF, v, a.v_stride, c0, s.nk);
+        }
+        copies_commit();
+    };
+    stage_rows<D, ROWS, THREADS>(sq, static_cast<const float *>(a.q) + s.q0 * a.q_stride + (int64_t)h * D, a.q_stride, r0,
+                                 s.nq);
+    stage_rows<D, ROWS, THREADS>(sg, static_cast<const float *>(a.d_out) + (s.q0 * a.bt.Hq + h) * (int64_t)D,
+                                 (int64_t)a.bt.Hq * D, r0, s.nq);
+    load(0, 0);
+    stage_stats<ROWS, THREADS>(stats, stats + kPT, a, s, r0, h);
+    const float sc = a.scale * kLog2e;
     float gq[4][D / 16] = {};
-    const int end = keys_seen(s, min(r0 + kPT, s.nq) - 1, a.causal);
-    for (int c0 = 0; c0 < end; c0 += kPT) {
+    int at = 0;
+    for (int c0 = 0; c0 < end; c0 += kPT, at ^= 1) {
+        copies_wait();
         __syncthreads();
-        stage_rows<T, D>(sk, k, a.k_stride, c0, s.nk, 1.f);
-        stage_rows<T, D>(sv, v, a.v_stride, c0, s.nk, 1.f);
-        __syncthreads();
+        load(c0 + kPT, at ^ 1);
+        const float *sk = ring + 2 * at * C::kTileF, *sv = sk + C::kTileF;
         float x[4][4] = {}, y[4][4] = {};
         dot_rows<D>(x, sq, sk, ty, tx);
         dot_rows<D>(y, sg, sv, ty, tx);
-        grad_scores(x, y, s, lse2, delta, r0, c0, ty, tx, a.causal, false);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sp[(4 * ty + i) * 68 + tx + 16 * j] = y[i][j];
-        __syncwarp();
+            for (int j = 0; j < 4; ++j) x[i][j] *= sc;
+        grad_scores(x, y, s, stats, stats + kPT, r0, c0, ty, tx, a.causal, false);
+        put_weights(sp, y, ty, tx);
         weigh_rows<D>(gq, sp, sk, ty, tx);
     }
+    copies_wait();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + 4 * ty + i;
-        if (r < s.nq)
-            write_row<T, D>(static_cast<T *>(a.dq) + ((s.q0 + r) * a.bt.Hq + h) * D, gq[i], tx, a.scale);
+        if (r < s.nq) write_row<D>(static_cast<float *>(a.dq) + ((s.q0 + r) * a.bt.Hq + h) * D, gq[i], tx, a.scale);
     }
 }
 
@@ -371,41 +412,63 @@ template <typename K> cudaError_t allow_smem(K kern, int bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <typename T, int D> cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t st) {
-    const int64_t tiles = max_tiles(a.bt.cu_q, a.bt.n, a.bt.Tq, kPT);
-    if (tiles == 0) return cudaSuccess;
-    constexpr int smem = prompt_smem<D>(3, 1);
-    cudaError_t e = allow_smem(attn_prompt_kernel<T, D>, smem);
+// Rows of a block: 64, or 16 where blocks of 64 rows would not reach every SM (a tile's work is then
+// spread over four times the blocks, and each is done sooner).
+inline int prompt_rows(const int32_t *cu, int n, int T, int heads, int sms) {
+    return max_tiles(cu, n, T, 64) * heads < sms ? 16 : 64;
+}
+
+template <int D, int ROWS> cudaError_t launch_prompt_rows(const PromptArgs &a, cudaStream_t st) {
+    const int64_t tiles = max_tiles(a.bt.cu_q, a.bt.n, a.bt.Tq, ROWS);
+    constexpr int smem = PromptCfg<D>::smem(ROWS, 1);
+    cudaError_t e = allow_smem(attn_prompt_kernel<D, ROWS>, smem);
     if (e != cudaSuccess) return e;
-    attn_prompt_kernel<T, D><<<dim3((unsigned)tiles, a.bt.Hq), kPThreads, smem, st>>>(a);
+    attn_prompt_kernel<D, ROWS><<<dim3((unsigned)tiles, a.bt.Hq), ROWS * 4, smem, st>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T, int D> cudaError_t launch_delta(const PromptArgs &a, cudaStream_t st) {
-    constexpr int LANES = D / Vec16<T>::N;
+template <int D> cudaError_t launch_prompt(const PromptArgs &a, int sms, cudaStream_t st) {
+    if (a.bt.Tq == 0) return cudaSuccess;
+    return prompt_rows(a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq, sms) == 16 ? launch_prompt_rows<D, 16>(a, st)
+                                                                       : launch_prompt_rows<D, 64>(a, st);
+}
+
+template <int D> cudaError_t launch_delta(const PromptArgs &a, cudaStream_t st) {
+    constexpr int LANES = D / 4;
     const int64_t rows = a.bt.cu_q ? 1 : a.bt.n;
     const int64_t items_q = rows * a.bt.Tq * a.bt.Hq, items_k = a.bt.cu_k ? rows * a.bt.Tk * a.bt.Hkv : 0;
     const int64_t items = items_q > items_k ? items_q : items_k;
     if (items == 0) return cudaSuccess;
-    attn_delta_kernel<T, D><<<(unsigned)((items * LANES + 255) / 256), 256, 0, st>>>(a);
+    attn_delta_kernel<D><<<(unsigned)((items * LANES + 255) / 256), 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T, int D> cudaError_t launch_prompt_grad(const PromptArgs &a, cudaStream_t st) {
-    cudaError_t e = launch_delta<T, D>(a, st);
+template <int D, int ROWS> cudaError_t launch_grad_kv(const PromptArgs &a, cudaStream_t st) {
+    constexpr int smem = PromptCfg<D>::smem(ROWS, 2);
+    cudaError_t e = allow_smem(attn_grad_kv_kernel<D, ROWS>, smem);
     if (e != cudaSuccess) return e;
-    constexpr int smem = prompt_smem<D>(4, 1);
-    const int64_t tk = max_tiles(a.bt.cu_k, a.bt.n, a.bt.Tk, kPT), tq = max_tiles(a.bt.cu_q, a.bt.n, a.bt.Tq, kPT);
-    if (tk > 0) {
-        if ((e = allow_smem(attn_grad_kv_kernel<T, D>, smem)) != cudaSuccess) return e;
-        attn_grad_kv_kernel<T, D><<<dim3((unsigned)tk, a.bt.Hkv), kPThreads, smem, st>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    if (tq > 0) {
-        if ((e = allow_smem(attn_grad_q_kernel<T, D>, smem)) != cudaSuccess) return e;
-        attn_grad_q_kernel<T, D><<<dim3((unsigned)tq, a.bt.Hq), kPThreads, smem, st>>>(a);
-    }
+    const int64_t tiles = max_tiles(a.bt.cu_k, a.bt.n, a.bt.Tk, ROWS);
+    attn_grad_kv_kernel<D, ROWS><<<dim3((unsigned)tiles, a.bt.Hkv), ROWS * 4, smem, st>>>(a);
     return cudaGetLastError();
+}
+template <int D, int ROWS> cudaError_t launch_grad_q(const PromptArgs &a, cudaStream_t st) {
+    constexpr int smem = PromptCfg<D>::smem(ROWS, 2);
+    cudaError_t e = allow_smem(attn_grad_q_kernel<D, ROWS>, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = max_tiles(a.bt.cu_q, a.bt.n, a.bt.Tq, ROWS);
+    attn_grad_q_kernel<D, ROWS><<<dim3((unsigned)tiles, a.bt.Hq), ROWS * 4, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int D> cudaError_t launch_prompt_grad(const PromptArgs &a, int sms, cudaStream_t st) {
+    cudaError_t e = launch_delta<D>(a, st);
+    if (e == cudaSuccess && a.bt.Tk > 0)
+        e = prompt_rows(a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv, sms) == 16 ? launch_grad_kv<D, 16>(a, st)
+                                                                         : launch_grad_kv<D, 64>(a, st);
+    if (e == cudaSuccess && a.bt.Tq > 0)
+        e = prompt_rows(a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq, sms) == 16 ? launch_grad_q<D, 16>(a, st)
+                                                                        : launch_grad_q<D, 64>(a, st);
+    return e;
 }
 
 }  // namespace attn

@@ -90,14 +90,15 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     return d;
 }
 
-// 2^x of two numbers on the FMA units, for x <= 127 and not NaN: x = n + f with |f| <= 1/2, 2^f by the
+// 2^x of two numbers on the FMA units, for x <= 127: x = n + f with |f| <= 1/2, 2^f by the
 // polynomial of degree 5 with the least largest relative error (7.5e-8, found by exchange; 2.1e-7 as
-// evaluated, no more than the SFU's), n added to the exponent.  Below -126 it stays at 2^-126.
+// evaluated, no more than the SFU's), n added to the exponent.  Below -126 it stays at 2^-126;
+// NaN gives the largest number, infinite once rounded to bf16.
 // The SFU gives 16 powers a clock and SM, so a tile of 128 x 128 weights takes as long as its two
 // products of depth 128; taking a part of the powers here shortens the longer of the two.
 __device__ __forceinline__ float2 ex2_fma(float2 x) {
-    x.x = fmaxf(x.x, -126.f);
-    x.y = fmaxf(x.y, -126.f);
+    x.x = max3_nan(x.x, -126.f, -126.f);
+    x.y = max3_nan(x.y, -126.f, -126.f);
     constexpr float kRound = 12582912.f;   // 1.5 * 2^23: adding it rounds to a whole number
     const float2 y = add2(x, make_float2(kRound, kRound));
     const float2 n = add2(y, make_float2(-kRound, -kRound));
