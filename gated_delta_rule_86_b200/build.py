@@ -2,7 +2,8 @@
 
 ``build_library()`` compiles ``csrc/kda_api.cu`` (which includes every kernel)
 into ``libkda_b200.so`` next to this file.  The build is skipped when the
-library is newer than every source file.
+library is newer than every source file.  ``build_binding()`` compiles the native
+binding of the attention calls against torch's headers.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB_PATH = os.path.join(HERE, "libkda_b200.so")
+BINDING_PATH = os.path.join(HERE, "_attention.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH_FLAGS + ["-split-compile=0", "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared"]
 
@@ -50,6 +52,32 @@ def build_library(force: bool = False) -> str:
     return compile_so(os.path.join(HERE, "csrc", "kda_api.cu"), LIB_PATH, _sources(), force=force)
 
 
+def build_binding(force: bool = False) -> str:
+    """The native Python binding of the attention calls (g++, torch's headers), beside the library that it
+    links to."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    src = os.path.join(HERE, "csrc", "attn_binding.cpp")
+    if not (force or _stale(BINDING_PATH, [src, os.path.join(ROOT, "include", "kda.h")])):
+        return BINDING_PATH
+    build_library()
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DTORCH_API_INCLUDE_EXTENSION_H",
+           "-DTORCH_EXTENSION_NAME=_attention", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in include_paths() + [os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", d]
+    cmd += [src, "-o", tmp, f"-L{libs}", f"-L{HERE}", "-l:libkda_b200.so", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def build_probe(force: bool = False) -> str:
     """Test-only tcgen05 probe library (tests/csrc)."""
     src = os.path.join(ROOT, "tests", "csrc", "tc_probe.cu")
@@ -59,4 +87,5 @@ def build_probe(force: bool = False) -> str:
 
 if __name__ == "__main__":
     print(build_library(force=True))
+    print(build_binding(force=True))
     print(build_probe(force=True))

@@ -6,7 +6,7 @@ import torch
 
 import gated_delta_rule_86_b200 as kda
 from gated_delta_rule_86_b200 import _lib
-from gated_delta_rule_86_b200.attention import _tokens
+from gated_delta_rule_86_b200.attention import _native
 
 E, U, OK = _lib.KDA_ERR_INVALID_ARG, _lib.KDA_ERR_UNSUPPORTED, _lib.KDA_OK
 F = 1 << 20            # aligned, never dereferenced: every call below is rejected first
@@ -18,6 +18,7 @@ B16, F32 = _lib.KDA_BF16, _lib.KDA_F32
 def lib():
     from gated_delta_rule_86_b200 import build
     build.build_library()
+    build.build_binding()
     return _lib.load()
 
 
@@ -110,7 +111,7 @@ def test_status_name(lib):
     assert lib.kda_status_string(5).decode() == "KDA_ERR_BAD_PAGE"
 
 
-def test_binding_refuses():
+def test_binding_refuses(lib):
     x = torch.zeros(1, 4, 2, 64)
     i = torch.zeros(1, dtype=torch.int32)
     t = torch.zeros(1, 4, dtype=torch.int32)
@@ -138,10 +139,11 @@ def test_binding_refuses():
             call()
 
 
-def test_token_strides():
+def test_token_strides(lib):
     """Which layouts are read in place, and with which distance between tokens."""
+    _tokens = _native().tokens
     x = torch.zeros(3, 5, 8, 64)
-    assert _tokens(x)[1] == 512 and _tokens(x)[0] is x
+    assert _tokens(x)[1] == 512 and _tokens(x)[0].data_ptr() == x.data_ptr()
     part = x[:, :, 2:4]
     t, step = _tokens(part)
     assert t.data_ptr() == part.data_ptr() and step == 512
@@ -154,3 +156,21 @@ def test_token_strides():
     shifted = torch.zeros(3 * 5 * 8 * 64 + 1)[1:].view(3, 5, 8, 64)
     if shifted.data_ptr() % 16:
         assert _tokens(shifted)[0].data_ptr() % 16 == 0
+
+
+def test_missing_binding_fails_loudly(monkeypatch):
+    import gated_delta_rule_86_b200.attention as attention
+
+    def gone(*a):
+        raise ImportError("no such module")
+
+    monkeypatch.setattr(attention, "_module", None)
+    monkeypatch.setattr(attention.importlib, "import_module", gone)
+    with pytest.raises(ImportError, match="build_binding"):
+        kda.kda_attn_fwd(None, None, None)
+
+
+def test_status_becomes_kda_error(lib):
+    """The native module raises the package's own error type."""
+    err = kda.KdaError(2, "kda_attn_fwd")
+    assert err.status == 2 and "KDA_ERR_UNSUPPORTED" in str(err) and isinstance(err, RuntimeError)

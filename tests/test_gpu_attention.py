@@ -595,3 +595,56 @@ def test_fresh_threads():
     torch.cuda.synchronize()
     assert torch.equal(got["fwd"], out) and torch.equal(got["dec"], dec)
     assert all(torch.equal(a, b) for a, b in zip(got["bwd"], want))
+
+
+def test_refusals_name_their_status():
+    q = make((1, 8, 2, 96), 800, BF16)
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_attn_fwd(q, q, q)
+    assert e.value.status == 2
+    q = make((1, 8, 2, 64), 801, BF16)
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_attn_fwd(q, q, q, scale=0.0)
+    assert e.value.status == 1
+    kc = make((4, 2, 24, 64), 802, BF16)
+    table = torch.zeros((1, 2), dtype=torch.int32, device="cuda")
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_attn_decode_step(q[:, 0], kc, kc, table, table[0, :1])
+    assert e.value.status == 2
+
+
+def test_gradient_is_taken_once():
+    q = make((1, 40, 2, 64), 810, BF16).requires_grad_()
+    k = make((1, 40, 1, 64), 811, BF16)
+    out = kda.kda_attn(q, k, k)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        torch.autograd.grad(out.float().sum(), q, create_graph=True)
+    # only what needs a gradient gets one, and through several uses they add up
+    out = kda.kda_attn(q, k, k)
+    (out.float().sum() + out.float().sum()).backward()
+    once = torch.autograd.grad(kda.kda_attn(q, k, k).float().sum(), q)[0]
+    assert k.grad is None
+    # twice the upstream gradient is exact in bf16
+    assert torch.equal(q.grad, 2 * once)
+
+
+def test_gradient_in_a_graph_beside_an_eager_one():
+    """A gradient captured through the direct calls while an eager graph of the same leaves lives."""
+    q, k, v = (make((1, 130, h, 64), 820 + i, BF16).requires_grad_() for i, h in enumerate((4, 2, 2)))
+    g = make(q.shape, 825, BF16)
+    alive = kda.kda_attn(q, k, v)
+    qd, kd, vd = (t.detach() for t in (q, k, v))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out, lse = kda.kda_attn_fwd(qd, kd, vd, return_lse=True)
+        kda.kda_attn_bwd(qd, kd, vd, out, lse, g)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = kda.kda_attn_fwd(qd, kd, vd, return_lse=True)
+        got = kda.kda_attn_bwd(qd, kd, vd, out, lse, g)
+    graph.replay()
+    want = torch.autograd.grad(alive, (q, k, v), g)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda.synchronize()
