@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(kAppendThreads) attn_append_kernel(const Appen
 
     const int tid = threadIdx.x;
     const int64_t t0 = (int64_t)blockIdx.x * TOKENS;
+    next_may_start();
+    wait_for_previous();
     if (tid < TOKENS) {
         const int64_t t = t0 + tid;
         int seq = -1, pos = 0;
@@ -184,12 +186,9 @@ __global__ void __launch_bounds__(kAppendThreads) attn_append_kernel(const Appen
 template <typename T, int D> cudaError_t launch_append_d(const AppendArgs &a, cudaStream_t st) {
     // few tokens: one per block, so that they spread over the SMs; many: four, whose sines (up to 64
     // each) keep all 256 threads busy at once
-    if (a.tokens <= 148 * 8) {
-        attn_append_kernel<T, D, 1><<<(unsigned)a.tokens, kAppendThreads, 0, st>>>(a);
-    } else {
-        attn_append_kernel<T, D, 4><<<(unsigned)((a.tokens + 3) / 4), kAppendThreads, 0, st>>>(a);
-    }
-    return cudaGetLastError();
+    if (a.tokens <= 148 * 8)
+        return launch_behind(attn_append_kernel<T, D, 1>, (unsigned)a.tokens, kAppendThreads, 0, st, a);
+    return launch_behind(attn_append_kernel<T, D, 4>, (unsigned)((a.tokens + 3) / 4), kAppendThreads, 0, st, a);
 }
 
 }  // namespace attn

@@ -13,6 +13,28 @@ namespace attn {
 // is longer than its row of the table (mirrors KDA_ERR_BAD_PAGE).
 constexpr int kDevErrBadPage = 5;
 
+// Kernels of this family are launched so that they may start while the one before them in the stream still
+// runs (programmatic dependent launch): their blocks come up, set up what is theirs alone, and wait there for
+// the end of what is before them, ahead of their first access to memory.  A decode step's kernels are so
+// short that coming up is a third of their time.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... A, typename... B>
+cudaError_t launch_behind(void (*kern)(A...), unsigned grid, int threads, size_t smem, cudaStream_t st, const B &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // The batch of a prompt call.  Dense: sequence n is row n of [B, T].  Packed (cu given): B == 1 and
 // sequence n is tokens cu[n] .. cu[n + 1] - 1.
 struct Batch {

@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kStages * C::kStageBytes;
     const uint8_t *ring_ptr = smem + warp * C::kStages * C::kStageBytes;
 
-    asm volatile("griddepcontrol.launch_dependents;");   // the join may take its place; it waits for this grid's end
+    next_may_start();
+    wait_for_previous();
     Walk<C::kTile> w;
     const bool work = w.start(a, scratch);
     if (a.per_pair && tid == 0) check_len(a, w.b);
@@ -453,6 +454,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
     constexpr int CPL = D / 32;   // channels of a lane
     __shared__ int64_t scratch[20];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x / a.vheads, vh = blockIdx.x % a.vheads;
+    next_may_start();
+    wait_for_previous();
     int64_t all = 0, before = 0;
     for (int n = tid; n < a.n; n += blockDim.x) {
         const int t = decode_units<TILE>(a, n);
@@ -464,7 +467,6 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
     const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv, hkv = vh / chunks, h0 = hkv * group + (vh % chunks) * GC;
     const int nh = min(GC, hkv * group + group - h0);
     const int tiles = decode_tiles<TILE>(a, b);
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the main kernel's parts, from here on
     if (tid == 0 && vh == 0) check_len(a, b);
     if (tiles == 0) {
         write_empty<T, D, GC>(a, b, vh);
@@ -504,23 +506,6 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
             static_cast<T *>(a.out)[h * D + lane * CPL + c] = from_f32<T>(sum > 0.f || sum != sum ? acc[c] / sum : 0.f);
         if (lane == 0 && a.lse) a.lse[h] = sum == 0.f ? -CUDART_INF_F : top * 0.69314718055994531f + logf(sum);
     }
-}
-
-// Launches a kernel that may start while the one before it in the stream still runs, and waits for it
-// itself (griddepcontrol.wait).
-template <typename... A, typename... B>
-cudaError_t launch_behind(void (*kern)(A...), unsigned grid, int threads, size_t smem, cudaStream_t st, const B &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 constexpr int kMaxDecodeBlocks = 1024;

@@ -89,7 +89,8 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
     const int gr = lane >> 2, gc = lane & 3;   // a fragment's row and column pair
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kStages * C::kStageBytes;
 
-    asm volatile("griddepcontrol.launch_dependents;");   // the join may take its place; it waits for this grid's end
+    next_may_start();
+    wait_for_previous();
     Walk<C::kTile> w;
     const bool work = w.start(a, scratch);
     if (a.per_pair && tid == 0) check_len(a, w.b);
@@ -345,8 +346,8 @@ template <typename T, int D, int GC, typename C> cudaError_t launch_decode_g(voi
     const int64_t pairs = (int64_t)a.n * a.vheads, tokens = (int64_t)a.cache.width << a.cache.page_log2;
     a.per_pair = decode_per_pair(pairs, tokens, sms);
     a.blocks = a.per_pair ? (int)pairs : decode_blocks(a, C::kTile, sms);
-    kern<<<a.blocks, threads, C::kSmem, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.per_pair) return e;
+    e = launch_behind(kern, (unsigned)a.blocks, threads, C::kSmem, st, a);
+    if (e != cudaSuccess || a.per_pair) return e;
     return launch_behind(attn_decode_join_kernel<T, D, GC, C::kTile>, (unsigned)pairs, kJoinThreads, 0, st, a);
 }
 

@@ -210,18 +210,24 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
     const uint32_t sbase = tc::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    next_may_start();
+    const uint32_t tmem = grad_setup<D>(bars, 17);
+    if (tid == 32) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&maps.g);
+    wait_for_previous();
     zero_behind<D>(static_cast<__nv_bfloat16 *>(a.dk), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv);
     zero_behind<D>(static_cast<__nv_bfloat16 *>(a.dv), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv);
     // the first keys of a sequence are seen by the most queries: they go first
     int n, t;
-    if (!find_tile(a.bt.cu_k, a.bt.n, a.bt.Tk, kTile, blockIdx.x / a.bt.Hkv, bars.scratch, n, t)) return;
+    if (!find_tile(a.bt.cu_k, a.bt.n, a.bt.Tk, kTile, blockIdx.x / a.bt.Hkv, bars.scratch, n, t)) {
+        if (warp == 16) tc::tmem_dealloc(tmem, 512);
+        return;
+    }
     const Seq s = seq_of(a.bt, n);
     const int hk = blockIdx.x % a.bt.Hkv, c0 = t * kTile, group = a.bt.Hq / a.bt.Hkv;
     const int ahead = s.nk - s.nq;   // causal: query i sees keys j <= i + ahead
     const int start = a.causal ? max(0, c0 - ahead) / kTile : 0;
     const int per_head = max(0, (s.nq + kTile - 1) / kTile - start), total = per_head * group;
 
-    const uint32_t tmem = grad_setup<D>(bars, 17);
     volatile int *abort = &bars.abort;
     const uint32_t tS = tmem, tP = tmem + kTile, tV = tmem + 2 * kTile, tK = tV + D;
     float *stats = reinterpret_cast<float *>(smem + C::kStats);
@@ -421,15 +427,21 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
     const uint32_t sbase = tc::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    next_may_start();
+    const uint32_t tmem = grad_setup<D>(bars, 16);
+    if (tid == 32) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&maps.g), prefetch_map(&maps.o);
+    wait_for_previous();
     zero_behind<D>(static_cast<__nv_bfloat16 *>(a.dq), a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq);
     const int64_t tiles = gridDim.x / a.bt.Hq;
     int n, t;
-    if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, kTile, tiles - 1 - blockIdx.x / a.bt.Hq, bars.scratch, n, t)) return;
+    if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, kTile, tiles - 1 - blockIdx.x / a.bt.Hq, bars.scratch, n, t)) {
+        if (warp == 16) tc::tmem_dealloc(tmem, 512);
+        return;
+    }
     const Seq s = seq_of(a.bt, n);
     const int h = blockIdx.x % a.bt.Hq, hk = h / (a.bt.Hq / a.bt.Hkv), r0 = t * kTile;
     const int total = (keys_seen(s, min(r0 + kTile, s.nq) - 1, a.causal) + kTile - 1) / kTile;
 
-    const uint32_t tmem = grad_setup<D>(bars, 16);
     volatile int *abort = &bars.abort;
     const uint32_t tS = tmem, tP = tmem + kTile, tQ = tmem + 3 * kTile;
 
@@ -588,14 +600,14 @@ template <int D> cudaError_t launch_prompt_grad_tc(const PromptArgs &a, cudaStre
     PromptMaps maps = {};
     if (a.bt.Tq > 0 && !encode_prompt_maps(maps, a, D)) return cudaErrorInvalidValue;
     if (gq > 0) {   // first: it forms the delta that the other reads
-        attn_grad_q_tc_kernel<D><<<(unsigned)gq, C::kThreads, C::kSmem, st>>>(a, maps);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_behind(attn_grad_q_tc_kernel<D>, (unsigned)gq, C::kThreads, C::kSmem, st, a, maps)) != cudaSuccess)
+            return e;
     }
     if (gk > 0) {
         if ((e = allow_smem(attn_grad_kv_tc_kernel<D>, C::kSmem)) != cudaSuccess) return e;
-        attn_grad_kv_tc_kernel<D><<<(unsigned)gk, C::kThreads, C::kSmem, st>>>(a, maps);
+        return launch_behind(attn_grad_kv_tc_kernel<D>, (unsigned)gk, C::kThreads, C::kSmem, st, a, maps);
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace attn

@@ -174,6 +174,10 @@ __device__ __forceinline__ void chain_ts(uint32_t d, uint32_t x, uint64_t y, uin
         mma_ts(d, x + operand_col(kk), y + kk * 128, idesc, accumulate || kk > 0, leader);
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // A head's tile of 128 tokens in 64-column blocks.
 template <int D>
 __device__ __forceinline__ void tma_tile(uint32_t dst, uint8_t *smem, const CUtensorMap *map, int head, int64_t row,
@@ -264,12 +268,22 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
     const uint32_t sbase = tc::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    next_may_start();
+    if (tid == 32) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v);
+    if (warp == 16) {
+        tc::tmem_alloc(&bars.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    wait_for_previous();
     // the last tiles of a sequence have the most keys: they go first
     const int units = pair_heads ? a.bt.Hq / 2 : a.bt.Hq;
     const int rows = pair_heads ? kTile : 2 * kTile;
     const int64_t tiles = gridDim.x / units;
     int n, t;
-    if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, rows, tiles - 1 - blockIdx.x / units, bars.scratch, n, t)) return;
+    if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, rows, tiles - 1 - blockIdx.x / units, bars.scratch, n, t)) {
+        if (warp == 16) tc::tmem_dealloc(bars.tmem, 512);
+        return;
+    }
     TwoTiles w;
     w.s = seq_of(a.bt, n);
     {
@@ -300,10 +314,6 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
         }
         tc::mbar_init(&bars.drain, 1);
         tc::fence_mbar_init();
-    }
-    if (warp == 16) {
-        tc::tmem_alloc(&bars.tmem, 512);
-        tc::tmem_relinquish();
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -587,8 +597,7 @@ template <int D> cudaError_t launch_prompt_tc(const PromptArgs &a, cudaStream_t 
     if (e != cudaSuccess) return e;
     PromptMaps maps = {};
     if (!encode_prompt_maps(maps, a, D)) return cudaErrorInvalidValue;
-    attn_prompt_tc_kernel<D><<<(unsigned)grid, C::kThreads, C::kSmem, st>>>(a, maps, pair);
-    return cudaGetLastError();
+    return launch_behind(attn_prompt_tc_kernel<D>, (unsigned)grid, C::kThreads, C::kSmem, st, a, maps, pair);
 }
 
 }  // namespace attn
