@@ -243,7 +243,7 @@ kda_status kda_attn_fwd(const void *q, const void *k, const void *v, int64_t q_s
     const int sms = kda::device_sm_count();
     if (sms < 1) return KDA_ERR_CUDA;
     if (dtype == KDA_F32) return status_of(d == 64 ? launch_prompt<64>(a, sms, st) : launch_prompt<128>(a, sms, st));
-    return status_of(d == 64 ? launch_prompt_tc<64>(a, st) : launch_prompt_tc<128>(a, st));
+    return status_of(d == 64 ? launch_prompt_tc<64>(a, sms, st) : launch_prompt_tc<128>(a, sms, st));
 }
 
 kda_status kda_attn_bwd_workspace_size(int32_t B, int32_t Tq, int32_t Hq, size_t *bytes) {

@@ -126,6 +126,88 @@ __device__ __forceinline__ bool find_tile(const int32_t *cu, int nseq, int T, in
     return seq >= 0;
 }
 
+// The index-th tile in an order in which no tile comes before one of a higher level, the level of tile t of a
+// sequence being t + 1 (with causal masking: the number of key tiles that it sees): items of about the same
+// cost go out together, the largest first.  Gives the sequence, its number of tiles and the level; false if
+// there are fewer tiles.  A whole warp.
+__device__ __forceinline__ bool place_of(const int32_t *cu, int nseq, int T, int tile, int64_t index, int lane, int &seq,
+                                         int &count, int &level) {
+    if (cu == nullptr) {
+        count = (T + tile - 1) / tile;
+        if (index >= (int64_t)count * nseq) return false;
+        level = count - (int)(index / nseq);
+        seq = (int)(index % nseq);
+        return true;
+    }
+    constexpr int kHeld = 4;   // tile counts that a lane keeps: the levels are searched for up to 128 sequences
+    int c[kHeld];
+    auto tiles_of = [&](int n) {
+        int64_t first;
+        int len = 0;
+        if (n < nseq) seq_range(cu, n, T, first, len);
+        return (len + tile - 1) / tile;
+    };
+    if (nseq > 32 * kHeld) {   // in the sequences' own order, each from its end
+        int64_t before = 0;
+        for (int n0 = 0; n0 < nseq; n0 += 32) {
+            const int mine = tiles_of(n0 + lane);
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            const int64_t end = before + upto;
+            const uint32_t hit = __ballot_sync(0xffffffffu, index >= end - mine && index < end);
+            if (hit) {
+                const int at = __ffs(hit) - 1;
+                seq = n0 + at;
+                count = __shfl_sync(0xffffffffu, mine, at);
+                level = (int)(__shfl_sync(0xffffffffu, end, at) - index);
+                return true;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        return false;
+    }
+    int top = 0;
+#pragma unroll
+    for (int x = 0; x < kHeld; ++x) {
+        c[x] = tiles_of(x * 32 + lane);
+        top = max(top, c[x]);
+    }
+    top = __reduce_max_sync(0xffffffffu, (unsigned)top);
+    auto above = [&](int l) {   // tiles of a level above l
+        int sum = 0;
+#pragma unroll
+        for (int x = 0; x < kHeld; ++x) sum += max(0, c[x] - l);
+        return (int64_t)__reduce_add_sync(0xffffffffu, sum);
+    };
+    if (index >= above(0)) return false;
+    int lo = 0, hi = top;   // above(lo) > index >= above(hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (above(mid) > index) lo = mid;
+        else hi = mid;
+    }
+    level = hi;
+    int k = (int)(index - above(hi));   // the k-th sequence with that level
+#pragma unroll
+    for (int x = 0; x < kHeld; ++x) {
+        uint32_t have = __ballot_sync(0xffffffffu, c[x] >= level);
+        const int number = __popc(have);
+        if (k < number) {
+            for (; k > 0; --k) have &= have - 1;
+            const int at = __ffs(have) - 1;
+            seq = x * 32 + at;
+            count = __shfl_sync(0xffffffffu, c[x], at);
+            return true;
+        }
+        k -= number;
+    }
+    return false;
+}
+
 // Keys [lo, hi) that some query of rows [r0, r1) of a sequence sees: with causal masking query i sees
 // keys j <= i + nk - nq, so that the last query sees the last key.
 __device__ __forceinline__ int keys_seen(const Seq &s, int row, bool causal) {

@@ -3,7 +3,8 @@
 //     S = Q K^T,   P = 2^(c S - c m),   O = P V / rowsum(P),   c = scale log2(e),
 // one pass over the keys in tiles of 128 with a running row maximum m and sum.
 //
-// A block works on two tiles of 128 queries that share their keys and values: two heads of a group
+// One block per SM takes items in turn, the ones with the most keys first; an item is two tiles of 128
+// queries that share their keys and values: two heads of a group
 // (the same rows) where the group is even, two neighbouring row tiles of one head otherwise.  Both
 // products run on tcgen05 with fp32 accumulators in Tensor Memory: S (128 x 128) per tile, O (128 x d)
 // per tile.  Warp roles:
@@ -24,6 +25,9 @@
 // rarely, by the softmax warps themselves: S_i of a tile is issued after the previous O_i, and the
 // tensor pipe works in order, so a complete S_i means a complete O_i.  P is rounded once, to bf16, the
 // operand type of V; the sum takes the unrounded weights.
+//
+// The ring of loads runs on from item to item, and an item's first products start under the end of the one
+// before: a block per item cost 7.5 us (d = 64) to 9 us (128) of coming up and running dry, as much as 5 turns.
 //
 // Rows past the end of a sequence in its last tile are another sequence's (or whatever lies behind):
 // their scores are masked, and their values are zeroed in shared memory before the product, since a
@@ -64,6 +68,15 @@ __device__ __forceinline__ uint32_t operand_col(int kk) { return (kk >> 2) * 64 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ void st_shared(uint32_t addr, float x) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+__device__ __forceinline__ float ld_shared(uint32_t addr) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
 }
 
 // Two fp32 operations in one instruction.
@@ -236,28 +249,69 @@ template <int D> struct FwdCfg {
     static constexpr int kStages = D == 128 ? 5 : 8;
     static constexpr int kQ = 0;                          // two query tiles
     static constexpr int kRing = 2 * kTileBytes;
-    static constexpr int kBars = kRing + kStages * kTileBytes;
-    static constexpr int kTop = kBars + 512;              // row maxima: [2 tiles][2 halves][128]
-    static constexpr int kSmem = kTop + 2 * 2 * kTile * 4;
+    static constexpr int kTop = kRing + kStages * kTileBytes;   // row maxima: [2 tiles][2 halves][128]
+    static constexpr int kBars = kTop + 2 * 2 * kTile * 4;
+    static constexpr int kSmem = kBars + 512;
     static constexpr int kThreads = 640;
     static constexpr int kUp = 104, kDown = 64;           // launched with 96 each: 128 (4 * 104 + 64) = 640 * 96
     static_assert(4 * kUp + kDown <= 5 * 96, "registers");
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-struct FwdBars {
-    uint64_t q_full[2], full[8], empty[8], s_full[2], p_ready[2][2], o_full[2], drain;
-    uint32_t tmem;
-    int abort;
-    int scratch[34];
+// An item: two tiles of queries.
+struct TwoTiles {
+    int64_t q0, k0;                  // the sequence's first query and key
+    int nq, nk, both;                // both: the larger of blocks; -1: no more items
+    int head[2], r0[2], blocks[2];   // head, first row, tiles of keys that it sees
+    int hk;                          // head of the cache
 };
 
-// Which two tiles of queries a block has.
-struct TwoTiles {
-    Seq s;
-    int head[2], r0[2], blocks[2];   // head, first row, tiles of keys that it sees
-    int hk;
+struct FwdBars {
+    uint64_t q_full[2], q_empty[2], full[8], empty[8], s_full[2], p_ready[2][2], o_full[2], item_full[2], item_empty[2],
+        drain;
+    uint32_t tmem;
+    int abort;
+    TwoTiles item[2];
 };
+static_assert(sizeof(FwdBars) <= 512, "barriers");
+
+// A block's r-th item; a whole warp.  Blocks take items there and back, so that none has the largest of
+// every round.
+__device__ __forceinline__ TwoTiles item_of(const PromptArgs &a, int pair_heads, int r, int lane) {
+    const int units = pair_heads ? a.bt.Hq / 2 : a.bt.Hq, rows = pair_heads ? kTile : 2 * kTile;
+    const int64_t index = (int64_t)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    int n, count, level;
+    TwoTiles w;
+    w.both = -1;
+    if (!place_of(a.bt.cu_q, a.bt.n, a.bt.Tq, rows, index / units, lane, n, count, level)) return w;
+    const Seq s = seq_of(a.bt, n);
+    w.q0 = s.q0, w.k0 = s.k0, w.nq = s.nq, w.nk = s.nk;
+    const int u = (int)(index % units), t = level - 1;
+    w.both = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        w.head[i] = pair_heads ? 2 * u + i : u;
+        w.r0[i] = t * rows + (pair_heads ? 0 : i * kTile);
+        const int last = min(w.r0[i] + kTile, s.nq) - 1;
+        w.blocks[i] = w.r0[i] < s.nq ? (keys_seen(s, last, a.causal) + kTile - 1) / kTile : 0;
+        w.both = max(w.both, w.blocks[i]);
+    }
+    w.hk = w.head[0] / (a.bt.Hq / a.bt.Hkv);
+    return w;
+}
+
+// 32 numbers of a thread's row, rounded, to 64 bytes of global memory in two whole sectors at a time.
+__device__ __forceinline__ void store32(__nv_bfloat16 *dst, const float (&x)[32], float mul) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 16) {
+        uint32_t u[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) u[y] = pack_bf16(x[e + 2 * y] * mul, x[e + 2 * y + 1] * mul);
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + e), "r"(u[0]), "r"(u[1]),
+                     "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                     : "memory");
+    }
+}
 
 template <int D>
 __global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1)
@@ -274,35 +328,11 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
         tc::tmem_alloc(&bars.tmem, 512);
         tc::tmem_relinquish();
     }
-    wait_for_previous();
-    // the last tiles of a sequence have the most keys: they go first
-    const int units = pair_heads ? a.bt.Hq / 2 : a.bt.Hq;
-    const int rows = pair_heads ? kTile : 2 * kTile;
-    const int64_t tiles = gridDim.x / units;
-    int n, t;
-    if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, rows, tiles - 1 - blockIdx.x / units, bars.scratch, n, t)) {
-        if (warp == 16) tc::tmem_dealloc(bars.tmem, 512);
-        return;
-    }
-    TwoTiles w;
-    w.s = seq_of(a.bt, n);
-    {
-        const int u = blockIdx.x % units;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            w.head[i] = pair_heads ? 2 * u + i : u;
-            w.r0[i] = t * rows + (pair_heads ? 0 : i * kTile);
-            const int last = min(w.r0[i] + kTile, w.s.nq) - 1;
-            w.blocks[i] = w.r0[i] < w.s.nq ? (keys_seen(w.s, last, a.causal) + kTile - 1) / kTile : 0;
-        }
-        w.hk = w.head[0] / (a.bt.Hq / a.bt.Hkv);
-    }
-    const int blocks = max(w.blocks[0], w.blocks[1]);
-
     if (tid == 0) {
         bars.abort = 0;
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars.q_full[i], 1);
+            tc::mbar_init(&bars.q_empty[i], 1);
             tc::mbar_init(&bars.s_full[i], 1);
             tc::mbar_init(&bars.p_ready[i][0], 9);   // eight softmax warps and the loads'
             tc::mbar_init(&bars.p_ready[i][1], 8);
@@ -311,6 +341,10 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
         for (int i = 0; i < C::kStages; ++i) {
             tc::mbar_init(&bars.full[i], 1);
             tc::mbar_init(&bars.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bars.item_full[i], 1);
+            tc::mbar_init(&bars.item_empty[i], 19);   // sixteen softmax warps, products, loads, words
         }
         tc::mbar_init(&bars.drain, 1);
         tc::fence_mbar_init();
@@ -321,99 +355,152 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
     const uint32_t tmem = bars.tmem;
     volatile int *abort = &bars.abort;
     constexpr uint32_t kO = 256;
-    const int past = blocks * kTile - w.s.nk;   // rows of the last V tile behind the sequence's end
+    wait_for_previous();
+    // the block's r-th item, and the word that a warp is done with it
+    auto get_item = [&](int r) { return warp_wait(&bars.item_full[r & 1], (r >> 1) & 1, abort); };
+    auto done_item = [&](int r) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars.item_empty[r & 1]);
+    };
 
+    // Counts that run on from item to item give the barriers' turns: `base` of the loads (K_0, V_0, K_1, ...
+    // of an item; load k lies in stage k mod kStages), `turn[i]` of tile i's key tiles, `had[i]` of the
+    // items in which tile i has any.
     if (warp >= 16) {
         regs_down<C::kDown>();
-        if (warp == 17 && lane == 0 && blocks > 0) {
-            for (int i = 0; i < 2; ++i) {
-                if (w.blocks[i] == 0) continue;
-                tc::mbar_arrive_expect_tx(&bars.q_full[i], C::kTileBytes);
-                tma_tile<D>(C::kQ + i * C::kTileBytes, smem, &maps.q, w.head[i], w.s.q0 + w.r0[i], &bars.q_full[i]);
+        int base = 0, turn[2] = {0, 0}, had[2] = {0, 0};
+        bool ok = true;
+        auto advance = [&](int r) {
+            const TwoTiles &w = bars.item[r & 1];
+            base += 2 * w.both;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) turn[i] += w.blocks[i], had[i] += w.blocks[i] > 0;
+            done_item(r);
+        };
+        auto loaded = [&](int k) { return warp_wait(&bars.full[k % C::kStages], (k / C::kStages) & 1, abort); };
+        if (warp == 19) {
+            for (int r = 0;; ++r) {
+                const TwoTiles w = item_of(a, pair_heads, r, lane);
+                if (r >= 2 && !warp_wait(&bars.item_empty[r & 1], ((r >> 1) - 1) & 1, abort)) break;
+                if (lane == 0) {
+                    bars.item[r & 1] = w;
+                    tc::mbar_arrive(&bars.item_full[r & 1]);
+                }
+                if (w.both < 0) break;
             }
-            int st = 0, put = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int j = 0; j < 2 * blocks; ++j) {   // K_0, V_0, K_1, ...
-                if (put >= C::kStages && !(ok = tc::mbar_wait(&bars.empty[st], ph ^ 1, abort))) break;
-                tc::mbar_arrive_expect_tx(&bars.full[st], C::kTileBytes);
-                tma_tile<D>(C::kRing + st * C::kTileBytes, smem, j & 1 ? &maps.v : &maps.k, w.hk,
-                            w.s.k0 + (int64_t)(j >> 1) * kTile, &bars.full[st]);
-                ++put;
-                if (++st == C::kStages) st = 0, ph ^= 1;
+        } else if (warp == 17) {
+            int put = 0, put_q[2] = {0, 0};   // loads under way
+            for (int r = 0; ok && (ok = get_item(r)) && bars.item[r & 1].both >= 0; ++r) {
+                const TwoTiles w = bars.item[r & 1];
+                for (int j = 0; j < 2 * w.both && ok; ++j) {
+                    const int k = base + j, st = k % C::kStages;
+                    if (j == min(2, 2 * w.both - 1)) {   // Q, once its place is free; the first keys need not wait for that
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (!ok || w.blocks[i] == 0) continue;
+                            if (had[i] > 0 && !(ok = warp_wait(&bars.q_empty[i], (had[i] - 1) & 1, abort))) continue;
+                            if (lane == 0) {
+                                tc::mbar_arrive_expect_tx(&bars.q_full[i], C::kTileBytes);
+                                tma_tile<D>(C::kQ + i * C::kTileBytes, smem, &maps.q, w.head[i], w.q0 + w.r0[i],
+                                            &bars.q_full[i]);
+                            }
+                            ++put_q[i];
+                        }
+                        if (!ok) break;
+                    }
+                    if (k >= C::kStages && !(ok = warp_wait(&bars.empty[st], (k / C::kStages - 1) & 1, abort))) break;
+                    if (lane == 0) {
+                        tc::mbar_arrive_expect_tx(&bars.full[st], C::kTileBytes);
+                        tma_tile<D>(C::kRing + st * C::kTileBytes, smem, j & 1 ? &maps.v : &maps.k, w.hk,
+                                    w.k0 + (int64_t)(j >> 1) * kTile, &bars.full[st]);
+                    }
+                    put = k + 1;
+                }
+                advance(r);
             }
-            if (!ok) {   // a wait ran out: leave no copy in flight
+            if (!ok && lane == 0) {   // a wait ran out: leave no copy in flight (each wait is bounded)
                 int quit = 0;
-                for (int i = 0; i < 2; ++i)
-                    if (w.blocks[i]) tc::mbar_wait(&bars.q_full[i], 0, &quit);
-                const int from = put > C::kStages ? put - C::kStages : 0;
-                for (int k = from; k < put; ++k) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    quit = 0;
+                    if (put_q[i] > 0) tc::mbar_wait(&bars.q_full[i], (put_q[i] - 1) & 1, &quit);
+                }
+                for (int k = max(0, put - C::kStages); k < put; ++k) {
                     quit = 0;
                     tc::mbar_wait(&bars.full[k % C::kStages], (k / C::kStages) & 1, &quit);
                 }
             }
         } else if (warp == 18) {
-            bool ok = true;
-            for (int j = 0; j < blocks && ok; ++j) {
-                const int kv = 2 * j + 1, kn = kv + 1;
-                const bool more = j + 1 < blocks;
-                if (!(ok = warp_wait(&bars.full[kv % C::kStages], (kv / C::kStages) & 1, abort))) break;
-                if (past > 0 && !more) {
-                    zero_rows<D>(smem + C::kRing + (kv % C::kStages) * C::kTileBytes, kTile - past, lane);
-                    __syncwarp();
+            for (int r = 0; ok && (ok = get_item(r)) && bars.item[r & 1].both >= 0; ++r) {
+                const TwoTiles w = bars.item[r & 1];
+                const int past = w.both * kTile - w.nk;   // rows of the last V tile behind the sequence's end
+                for (int j = 0; j < w.both && ok; ++j) {
+                    const int kv = base + 2 * j + 1;
+                    const bool more = j + 1 < w.both;
+                    if (!(ok = loaded(kv))) break;
+                    if (past > 0 && !more) {
+                        zero_rows<D>(smem + C::kRing + (kv % C::kStages) * C::kTileBytes, kTile - past, lane);
+                        __syncwarp();
+                    }
+                    if (more && !(ok = loaded(kv + 1))) break;
+                    if (lane == 0) {
+                        if (j < w.blocks[0]) tc::mbar_arrive(&bars.p_ready[0][0]);
+                        if (j < w.blocks[1]) tc::mbar_arrive(&bars.p_ready[1][0]);
+                    }
+                    // not ahead of the softmax: the next word belongs to the next turn
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (ok && j < w.blocks[i]) ok = warp_wait(&bars.p_ready[i][0], (turn[i] + j) & 1, abort);
                 }
-                if (more && !(ok = warp_wait(&bars.full[kn % C::kStages], (kn / C::kStages) & 1, abort))) break;
-                if (lane == 0) {
-                    if (j < w.blocks[0]) tc::mbar_arrive(&bars.p_ready[0][0]);
-                    if (j < w.blocks[1]) tc::mbar_arrive(&bars.p_ready[1][0]);
-                }
-                // not ahead of the softmax: the next word belongs to the next turn
-                for (int i = 0; i < 2 && ok; ++i)
-                    if (j < w.blocks[i]) ok = warp_wait(&bars.p_ready[i][0], j & 1, abort);
+                advance(r);
             }
-        } else if (warp == 16 && blocks > 0) {
+        } else if (warp == 16) {
             constexpr uint32_t idS = tc::make_idesc_bf16(kTile, kTile, false, false);
             constexpr uint32_t idO = tc::make_idesc_bf16(kTile, D, false, true);
             const uint32_t leader = elect_lane();
-            // load number k (K_0, V_0, K_1, ...) lies in stage k mod kStages
-            auto loaded = [&](int k) { return warp_wait(&bars.full[k % C::kStages], (k / C::kStages) & 1, abort); };
-            auto scores = [&](int i, int st) {
+            // S_i of key tile j, which is load k
+            auto scores = [&](int i, bool last, int k) {
                 chain_ss<D>(tmem + i * kTile, desc_k(sbase + C::kQ + i * C::kTileBytes, 0),
-                            desc_k(sbase + C::kRing + st * C::kTileBytes, 0), idS, leader);
+                            desc_k(sbase + C::kRing + (k % C::kStages) * C::kTileBytes, 0), idS, leader);
                 commit_by(&bars.s_full[i], leader);
+                if (last) commit_by(&bars.q_empty[i], leader);
             };
-            bool ok = loaded(0);
-            for (int i = 0; i < 2 && ok; ++i) {
-                if (w.blocks[i] == 0) continue;
-                ok = warp_wait(&bars.q_full[i], 0, abort);
-                if (ok) scores(i, 0);
-            }
-            if (ok) commit_by(&bars.empty[0], leader);
-            for (int j = 0; j < blocks && ok; ++j) {
-                const int kv = 2 * j + 1, kk1 = kv + 1;
-                const bool more = j + 1 < blocks;
+            for (int r = 0; ok && (ok = get_item(r)) && bars.item[r & 1].both >= 0; ++r) {
+                const int both = bars.item[r & 1].both, blocks[2] = {bars.item[r & 1].blocks[0], bars.item[r & 1].blocks[1]};
+                if (both > 0) ok = loaded(base);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (j >= w.blocks[i]) continue;
-                    const uint64_t v = desc_mn(sbase + C::kRing + (kv % C::kStages) * C::kTileBytes, 0);
+                    if (!ok || blocks[i] == 0) continue;
+                    ok = warp_wait(&bars.q_full[i], had[i] & 1, abort);
+                    if (ok) scores(i, blocks[i] == 1, base);
+                }
+                if (ok && both > 0) commit_by(&bars.empty[base % C::kStages], leader);
+                for (int j = 0; j < both && ok; ++j) {
+                    const int kv = base + 2 * j + 1;
 #pragma unroll
-                    for (int part = 0; part < 2 && ok; ++part) {   // the first 32 columns of either half, then the rest
-                        if (!(ok = warp_wait(&bars.p_ready[i][part], j & 1, abort))) break;
-                        tc::tc_fence_after();
+                    for (int i = 0; i < 2; ++i) {
+                        if (!ok || j >= blocks[i]) continue;
+                        const uint64_t v = desc_mn(sbase + C::kRing + (kv % C::kStages) * C::kTileBytes, 0);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int kk = (x >> 1) * 4 + part * 2 + (x & 1);
-                            mma_ts(tmem + kO + i * D, tmem + i * kTile + operand_col(kk), v + kk * 128, idO,
-                                   j > 0 || part + x > 0, leader);
+                        for (int part = 0; part < 2 && ok; ++part) {   // the first 32 columns of either half, then the rest
+                            if (!(ok = warp_wait(&bars.p_ready[i][part], (turn[i] + j) & 1, abort))) break;
+                            tc::tc_fence_after();
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const int kk = (x >> 1) * 4 + part * 2 + (x & 1);
+                                mma_ts(tmem + kO + i * D, tmem + i * kTile + operand_col(kk), v + kk * 128, idO,
+                                       j > 0 || part + x > 0, leader);
+                            }
                         }
+                        if (!ok) continue;
+                        if (j + 1 < blocks[i]) scores(i, j + 2 == blocks[i], kv + 1);
+                        else commit_by(&bars.o_full[i], leader);
                     }
                     if (!ok) break;
-                    if (j + 1 < w.blocks[i]) scores(i, kk1 % C::kStages);
-                    else commit_by(&bars.o_full[i], leader);
+                    commit_by(&bars.empty[kv % C::kStages], leader);
+                    if (j + 1 < both) commit_by(&bars.empty[(kv + 1) % C::kStages], leader);
                 }
-                if (!ok) break;
-                commit_by(&bars.empty[kv % C::kStages], leader);
-                if (more) commit_by(&bars.empty[kk1 % C::kStages], leader);
+                advance(r);
             }
             if (!ok) {   // no product in flight when the memory is given back
                 int quit = 0;
@@ -424,53 +511,60 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
         __syncwarp();
     } else {
         regs_up<C::kUp>();
-        const int i = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane, r = w.r0[i] + row;
+        const int i = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = tc::tmem_lane_base(warp), tS = tmem + i * kTile + half * 64 + lanes,
                        tO = tmem + kO + i * D + half * (D / 2) + lanes;
-        const int seen = (r < w.s.nq ? keys_seen(w.s, r, a.causal) : w.s.nk) - half * 64;
-        const int seen_all = keys_seen(w.s, min(w.r0[i] + quarter * 32, w.s.nq - 1), a.causal);   // by every row of the warp
         const float sc = a.scale * kLog2e;
-        const float lag = 8.f / sc;   // 2^8, in the scores' units
-        float *tops = reinterpret_cast<float *>(smem + C::kTop) + i * 2 * kTile + row;
+        const uint32_t tops = sbase + C::kTop + (i * 2 * kTile + row) * 4 + half * kTile * 4;   // this thread's place
         const uint32_t pair = 1 + i * 4 + quarter;   // barrier of the two warps that share rows
-        float m = -CUDART_INF_F, l = 0.f;
+        uint32_t turn = 0, had = 0;                  // parities
         bool ok = true;
-        for (int j = 0; j < w.blocks[i]; ++j) {
-            ok = warp_wait(&bars.s_full[i], j & 1, abort);
+        for (int round = 0; ok && (ok = get_item(round)) && bars.item[round & 1].both >= 0; ++round) {
+        const volatile TwoTiles &w = bars.item[round & 1];   // read where it is needed, not kept
+        const int blocks = w.blocks[i];
+        int seen, seen_all;   // keys that this row sees, less its half's begin; that every row of the warp sees
+        {
+            const int r0 = w.r0[i], nq = w.nq, nk = w.nk;
+            const Seq s{0, 0, nq, nk};
+            seen = (r0 + row < nq ? keys_seen(s, r0 + row, a.causal) : nk) - half * 64;
+            seen_all = keys_seen(s, min(r0 + quarter * 32, nq - 1), a.causal);
+        }
+        float m = -CUDART_INF_F, l = 0.f;
+        for (int j = 0; j < blocks; ++j) {
+            ok = warp_wait(&bars.s_full[i], turn, abort);
+            turn ^= 1;
             if (!ok) break;
             tc::tc_fence_after();
-            float x[2][32];
+            const int hidden = seen - j * kTile;   // columns from here on are
+            const bool masked = j * kTile + kTile > seen_all;
+            // the scores are read twice, for the maximum and for the powers: there are no registers to hold
+            // them in between
+            float mt = m;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tc::tmem_ld32(tS + c * 32, x[c]);
-            tc::tmem_ld_wait();
-            const int c0 = j * kTile;
-            const bool masked = c0 + kTile > seen_all;
-            if (masked) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 2; ++c) {
+                float x[32], top[4];
+                tc::tmem_ld32(tS + c * 32, x);
+                tc::tmem_ld_wait();
+                if (masked) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (c0 + c * 32 + e >= seen) x[c][e] = -CUDART_INF_F;
-            }
-            float top[4];
+                        if (c * 32 + e >= hidden) x[e] = -CUDART_INF_F;
+                }
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float *y = &x[c >> 1][(c & 1) * 16];
-                top[c] = max3_nan(y[0], y[1], y[2]);
-#pragma unroll
-                for (int e = 3; e < 15; e += 2) top[c] = max3_nan(top[c], y[e], y[e + 1]);
-                top[c] = max3_nan(top[c], y[15], y[15]);
+                for (int y = 0; y < 4; ++y) {
+                    const float *z = x + y * 8;
+                    top[y] = max3_nan(max3_nan(max3_nan(z[0], z[1], z[2]), z[3], z[4]), max3_nan(z[5], z[6], z[7]), z[7]);
+                }
+                mt = max3_nan(max3_nan(top[0], top[1], mt), top[2], top[3]);
             }
-            float mt = max3_nan(max3_nan(top[0], top[1], top[2]), top[3], m);
+            float x[2][16];
+            tc::tmem_ld16(tS, x[0]);
             // the row's other half.  It has read this one's by the next turn: the next scores wait for both's weights
-            tops[half * kTile] = mt;
+            st_shared(tops, mt);
             tc::named_sync(pair, 64);
-            {
-                const float other = tops[(half ^ 1) * kTile];
-                mt = max3_nan(mt, other, other);
-            }
+            mt = max3_nan(mt, ld_shared(tops ^ (kTile * 4)), m);
             // the maximum in use follows the true one when it is 2^8 behind (or is NaN)
-            const bool grow = !(mt <= m + lag);
+            const bool grow = !(mt * sc <= m * sc + 8.f);
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? ex2_approx((m - mt) * sc) : 1.f;
                 if (grow) m = mt;
@@ -492,14 +586,25 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
             const float base = m == -CUDART_INF_F ? 0.f : m == CUDART_INF_F ? CUDART_NAN_F : -m * sc;
             const float2 sc2 = make_float2(sc, sc), base2 = make_float2(base, base);
             float2 sum = make_float2(0.f, 0.f);
-            auto weights = [&](auto plain) {   // plain: nothing hidden, so a part of the powers may go to the FMA units
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t u[16];
+            for (int c = 0; c < 4; ++c) {   // 16 columns at a time, the next ones on their way
+                tc::tmem_ld_wait();
+                if (c < 3) tc::tmem_ld16(tS + (c + 1) * 16, x[(c + 1) & 1]);
+                float (&z)[16] = x[c & 1];
+                uint32_t u[8];
+                if (masked) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float2 y = fma2(make_float2(x[c][2 * e], x[c][2 * e + 1]), sc2, base2);
-                        if (plain.value && e % kEmulate == kEmulate - 1) {
+                    for (int e = 0; e < 8; ++e) {
+                        const float lo = c * 16 + 2 * e < hidden ? ex2_approx(fmaf(z[2 * e], sc, base)) : 0.f;
+                        const float hi = c * 16 + 2 * e + 1 < hidden ? ex2_approx(fmaf(z[2 * e + 1], sc, base)) : 0.f;
+                        sum = add2(sum, make_float2(lo, hi));
+                        u[e] = pack_bf16(lo, hi);
+                    }
+                } else {   // nothing hidden: a part of the powers goes to the FMA units
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float2 y = fma2(make_float2(z[2 * e], z[2 * e + 1]), sc2, base2);
+                        if (e % kEmulate == kEmulate - 1) {
                             y = ex2_fma(y);
                         } else {
                             y.x = ex2_approx(y.x);
@@ -508,49 +613,50 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                         sum = add2(sum, y);
                         u[e] = pack_bf16(y.x, y.y);
                     }
-                    tc::tmem_st16(tS + c * 16, u);
+                }
+                tc::tmem_st8(tS + c * 8, u);
+                if (c & 1) {   // half of the weights
                     tc::tmem_st_wait();
                     tc::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bars.p_ready[i][c]);
+                    if (lane == 0) tc::mbar_arrive(&bars.p_ready[i][c >> 1]);
                 }
-            };
-            if (masked) weights(std::false_type{});
-            else weights(std::true_type{});
+            }
             l += sum.x + sum.y;
         }
-        if (ok && w.blocks[i] > 0) ok = warp_wait(&bars.o_full[i], 0, abort);
-        if (ok) {   // the sum of the row's two halves (both scaled by the same m)
-            tops[half * kTile] = l;
-            tc::named_sync(pair, 64);
-            l += tops[(half ^ 1) * kTile];
-        } else {   // a wait ran out: the other warp may stand at the barrier
+        if (ok && blocks > 0) ok = warp_wait(&bars.o_full[i], had, abort);
+        if (!ok) {   // a wait ran out: the other warp may stand at the barrier
             asm volatile("bar.arrive %0, 64;" ::"r"(pair) : "memory");
+            break;
         }
-        const int rows_left = w.s.nq - (w.r0[i] + quarter * 32);
-        if (ok && rows_left > 0 && half == 0) {
-            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-            tc::tc_fence_after();
-            // Q_i's shared memory is free once O_i is complete
-            RowWriter<D> out{smem + C::kQ + i * C::kTileBytes + quarter * 32 * D * 2};
+        // the sum of the row's two halves (both scaled by the same m)
+        st_shared(tops, l);
+        tc::named_sync(pair, 64);
+        l += ld_shared(tops ^ (kTile * 4));
+        tc::named_sync(pair, 64);   // read, before the next item's maxima come
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        const int r = w.r0[i] + row, head = w.head[i];
+        const bool there = r < w.nq;
+        const int64_t at = w.q0 + r;
+        done_item(round);
+        tc::tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                if (w.blocks[i] > 0) {
-                    tc::tmem_ld32(tO + c * 32, o);
-                    tc::tmem_ld_wait();
-                }
-                if (w.blocks[i] == 0 || inv == 0.f) {   // nothing seen: zero, whatever the accumulator holds
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                }
-                out.put(lane, c, o, inv);
+        for (int c = 0; c < D / 64; ++c) {   // this half's columns
+            float o[32];
+            if (blocks > 0) {
+                tc::tmem_ld32(tO + c * 32, o);
+                tc::tmem_ld_wait();
             }
-            out.flush(lane, static_cast<__nv_bfloat16 *>(a.out) +
-                                ((w.s.q0 + w.r0[i] + quarter * 32) * a.bt.Hq + w.head[i]) * (int64_t)D,
-                      (int64_t)a.bt.Hq * D, rows_left);
-            if (a.lse && r < w.s.nq)
-                a.lse[stat_at(a.bt, w.s.q0 + r, w.head[i])] = l == 0.f ? -CUDART_INF_F : m * a.scale + logf(l);
+            if (blocks == 0 || inv == 0.f) {   // nothing seen: zero, whatever the accumulator holds
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            }
+            if (there)
+                store32(static_cast<__nv_bfloat16 *>(a.out) + (at * a.bt.Hq + head) * (int64_t)D + half * (D / 2) + c * 32, o,
+                        inv);
+        }
+        if (a.lse && half == 0 && there) a.lse[stat_at(a.bt, at, head)] = l == 0.f ? -CUDART_INF_F : m * a.scale + logf(l);
+        had ^= blocks > 0;
         }
     }
     tc::tc_fence_before();
@@ -584,20 +690,19 @@ inline bool encode_prompt_maps(PromptMaps &m, const PromptArgs &a, int d) {
                          encode_tile_map(&m.o, a.out, (int64_t)a.bt.Hq * d, d, a.bt.Hq, tq)));
 }
 
-template <int D> cudaError_t launch_prompt_tc(const PromptArgs &a, cudaStream_t st) {
+template <int D> cudaError_t launch_prompt_tc(const PromptArgs &a, int sms, cudaStream_t st) {
     using C = FwdCfg<D>;
     // two heads of a group share rows, keys and the number of key tiles; an odd group takes two row tiles
     const int pair = a.bt.Hq / a.bt.Hkv % 2 == 0;
     const int64_t tiles = max_tiles(a.bt.cu_q, a.bt.n, a.bt.Tq, pair ? kTile : 2 * kTile);
-    const int64_t grid = tiles * (pair ? a.bt.Hq / 2 : a.bt.Hq);
+    const int64_t grid = tiles * (pair ? a.bt.Hq / 2 : a.bt.Hq);   // items
     if (a.bt.Tq == 0 || grid == 0) return cudaSuccess;
-    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
     // before the maps: it binds the device's context to this thread, which their encoding needs
     const cudaError_t e = allow_smem(attn_prompt_tc_kernel<D>, C::kSmem);
     if (e != cudaSuccess) return e;
     PromptMaps maps = {};
     if (!encode_prompt_maps(maps, a, D)) return cudaErrorInvalidValue;
-    return launch_behind(attn_prompt_tc_kernel<D>, (unsigned)grid, C::kThreads, C::kSmem, st, a, maps, pair);
+    return launch_behind(attn_prompt_tc_kernel<D>, (unsigned)(grid < sms ? grid : sms), C::kThreads, C::kSmem, st, a, maps, pair);
 }
 
 }  // namespace attn
