@@ -45,16 +45,15 @@ template <int D> struct GradCfg {
 };
 
 struct GradBars {
-    uint64_t own_full, out_full, out_read, first, full[8], empty[8], stats[2], stats_read[2], s_full, dp_full[2], a_ready,
-        b_ready, done, drain;
+    uint64_t own_full, out_full, out_read, first, full[8], empty[8], stats[2], stats_read[2], s_full, dp_full[2], q_word,
+        a_ready, b_ready, done, drain;
     uint32_t tmem;
     int abort;
-    int scratch[34];
 };
 static_assert(sizeof(GradBars) <= 512, "barriers");
 
 // Barriers and Tensor Memory; every thread.  Returns the Tensor Memory's base.
-template <int D> __device__ __forceinline__ uint32_t grad_setup(GradBars &bars, int b_count) {
+template <int D> __device__ __forceinline__ uint32_t grad_setup(GradBars &bars, int a_count, int b_count) {
     using C = GradCfg<D>;
     if (threadIdx.x == 0) {
         bars.abort = 0;
@@ -73,7 +72,8 @@ template <int D> __device__ __forceinline__ uint32_t grad_setup(GradBars &bars, 
         tc::mbar_init(&bars.s_full, 1);
         tc::mbar_init(&bars.dp_full[0], 1);
         tc::mbar_init(&bars.dp_full[1], 1);
-        tc::mbar_init(&bars.a_ready, 17);   // sixteen compute warps and the next loads' word
+        tc::mbar_init(&bars.q_word, 1);
+        tc::mbar_init(&bars.a_ready, a_count);   // sixteen compute warps, and the next loads' word where it goes with them
         tc::mbar_init(&bars.b_ready, b_count);
         tc::mbar_init(&bars.done, 1);
         tc::mbar_init(&bars.drain, 1);
@@ -211,25 +211,30 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     next_may_start();
-    const uint32_t tmem = grad_setup<D>(bars, 17);
+    const uint32_t tmem = grad_setup<D>(bars, D == 64 ? 16 : 17, 17);
     if (tid == 32) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&maps.g);
     wait_for_previous();
     zero_behind<D>(static_cast<__nv_bfloat16 *>(a.dk), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv);
     zero_behind<D>(static_cast<__nv_bfloat16 *>(a.dv), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv);
     // the first keys of a sequence are seen by the most queries: they go first
-    int n, t;
-    if (!find_tile(a.bt.cu_k, a.bt.n, a.bt.Tk, kTile, blockIdx.x / a.bt.Hkv, bars.scratch, n, t)) {
+    int n;
+    int count, level;
+    if (!place_of(a.bt.cu_k, a.bt.n, a.bt.Tk, kTile, blockIdx.x / a.bt.Hkv, lane, n, count, level)) {
         if (warp == 16) tc::tmem_dealloc(tmem, 512);
         return;
     }
     const Seq s = seq_of(a.bt, n);
-    const int hk = blockIdx.x % a.bt.Hkv, c0 = t * kTile, group = a.bt.Hq / a.bt.Hkv;
+    const int hk = blockIdx.x % a.bt.Hkv, c0 = (count - level) * kTile, group = a.bt.Hq / a.bt.Hkv;
     const int ahead = s.nk - s.nq;   // causal: query i sees keys j <= i + ahead
     const int start = a.causal ? max(0, c0 - ahead) / kTile : 0;
     const int per_head = max(0, (s.nq + kTile - 1) / kTile - start), total = per_head * group;
 
     volatile int *abort = &bars.abort;
-    const uint32_t tS = tmem, tP = tmem + kTile, tV = tmem + 2 * kTile, tK = tV + D;
+    const uint32_t tP = tmem + kTile, tV = tmem + 2 * kTile, tK = tV + D;
+    // With d = 64 there is Tensor Memory for the next turn's scores beside this one's: they are formed ahead,
+    // and the powers of a turn follow the dS of the one before without a product in between.
+    constexpr bool kAhead = D == 64;
+    auto tS = [&](int it) { return kAhead && (it & 1) ? tK + D : tmem; };
     float *stats = reinterpret_cast<float *>(smem + C::kStats);
     // turn `it` is query tile r0 of head h; its Q is load 2 it, its dO load 2 it + 1
     auto head_of = [&](int it) { return hk * group + it / per_head; };
@@ -290,7 +295,11 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
                     if (x == 1 && lane == 0) tc::mbar_arrive(&bars.first);
                     continue;
                 }
-                uint64_t *word = x ? &bars.b_ready : &bars.a_ready;
+                if (kAhead && x == 0) {   // a word of its own, not before the one before it has been heard
+                    if (it == total) continue;
+                    if (it > 1 && !(ok = warp_wait(&bars.s_full, (it - 1) & 1, abort))) break;
+                }
+                uint64_t *word = x ? &bars.b_ready : kAhead ? &bars.q_word : &bars.a_ready;
                 if (lane == 0) tc::mbar_arrive(word);
                 if (x == 1) ok = warp_wait(&bars.b_ready, (it - 1) & 1, abort);   // a_ready's turn is over, too
             }
@@ -304,7 +313,7 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
         if (total > 0) {
             ok = warp_wait(&bars.own_full, 0, abort) && warp_wait(&bars.first, 0, abort);
             if (ok) {
-                chain_ss<D>(tS, desc_k(sK, 0), desc_k(sbase + stage_of<D>(0), 0), idS, leader);
+                chain_ss<D>(tS(0), desc_k(sK, 0), desc_k(sbase + stage_of<D>(0), 0), idS, leader);
                 commit_by(&bars.s_full, leader);
                 chain_ss<D>(tP, desc_k(sV, 0), desc_k(sbase + stage_of<D>(1), 0), idS, leader);
                 commit_by(&bars.dp_full[0], leader);
@@ -312,13 +321,18 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
         }
         for (int it = 0; it < total && ok; ++it) {
             const bool more = it + 1 < total;
+            auto next_scores = [&]() {
+                chain_ss<D>(tS(it + 1), desc_k(sK, 0), desc_k(sbase + stage_of<D>(2 * it + 2), 0), idS, leader);
+                commit_by(&bars.s_full, leader);
+            };
+            if (kAhead && more) {
+                if (!(ok = warp_wait(&bars.q_word, it & 1, abort))) break;
+                next_scores();
+            }
             if (!(ok = warp_wait(&bars.a_ready, it & 1, abort))) break;
             tc::tc_fence_after();
-            chain_ts32(tV, tS, desc_mn(sbase + stage_of<D>(2 * it + 1), 0), idG, it > 0, leader);
-            if (more) {
-                chain_ss<D>(tS, desc_k(sK, 0), desc_k(sbase + stage_of<D>(2 * it + 2), 0), idS, leader);
-                commit_by(&bars.s_full, leader);
-            }
+            chain_ts32(tV, tS(it), desc_mn(sbase + stage_of<D>(2 * it + 1), 0), idG, it > 0, leader);
+            if (!kAhead && more) next_scores();
             commit_by(&bars.empty[stage_no<D>(2 * it + 1)], leader);
             if (!(ok = warp_wait(&bars.b_ready, it & 1, abort))) break;
             tc::tc_fence_after();
@@ -352,7 +366,7 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
             float2 p[16];
             {
                 float x[32];
-                tc::tmem_ld32(tS + lanes, x);
+                tc::tmem_ld32(tS(it) + lanes, x);
                 tc::tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
@@ -370,7 +384,7 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
                     if (2 * e + 1 < from) p[e].y = 0.f;
                 }
             }
-            put_operand(tS + lanes, p);
+            put_operand(tS(it) + lanes, p);
             arrive_operand(&bars.a_ready, lane);
             ok = warp_wait(&bars.dp_full[0], it & 1, abort);
             if (!ok) break;
@@ -428,18 +442,17 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     next_may_start();
-    const uint32_t tmem = grad_setup<D>(bars, 16);
+    const uint32_t tmem = grad_setup<D>(bars, 17, 16);
     if (tid == 32) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&maps.g), prefetch_map(&maps.o);
     wait_for_previous();
     zero_behind<D>(static_cast<__nv_bfloat16 *>(a.dq), a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq);
-    const int64_t tiles = gridDim.x / a.bt.Hq;
-    int n, t;
-    if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, kTile, tiles - 1 - blockIdx.x / a.bt.Hq, bars.scratch, n, t)) {
+    int n, count, level;
+    if (!place_of(a.bt.cu_q, a.bt.n, a.bt.Tq, kTile, blockIdx.x / a.bt.Hq, lane, n, count, level)) {
         if (warp == 16) tc::tmem_dealloc(tmem, 512);
         return;
     }
     const Seq s = seq_of(a.bt, n);
-    const int h = blockIdx.x % a.bt.Hq, hk = h / (a.bt.Hq / a.bt.Hkv), r0 = t * kTile;
+    const int h = blockIdx.x % a.bt.Hq, hk = h / (a.bt.Hq / a.bt.Hkv), r0 = (level - 1) * kTile;
     const int total = (keys_seen(s, min(r0 + kTile, s.nq) - 1, a.causal) + kTile - 1) / kTile;
 
     volatile int *abort = &bars.abort;
