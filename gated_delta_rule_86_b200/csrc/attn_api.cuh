@@ -280,7 +280,7 @@ kda_status kda_attn_bwd(const void *q, const void *k, const void *v, int64_t q_s
     if (sms < 1) return KDA_ERR_CUDA;
     if (dtype == KDA_F32)
         return status_of(d == 64 ? launch_prompt_grad<64>(a, sms, st) : launch_prompt_grad<128>(a, sms, st));
-    return status_of(d == 64 ? launch_prompt_grad_tc<64>(a, st) : launch_prompt_grad_tc<128>(a, st));
+    return status_of(d == 64 ? launch_prompt_grad_tc<64>(a, sms, st) : launch_prompt_grad_tc<128>(a, sms, st));
 }
 
 }  // extern "C"

@@ -132,9 +132,23 @@ __device__ __forceinline__ float2 ex2_fma(float2 x) {
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
+// Waits for a turn of a barrier to complete, at most kWaitLimit polls (some tenths of a second to a few
+// seconds, where a healthy wait takes microseconds); then records the error, tells the block (*abort) and
+// returns false, as it does once the block has been told.
+constexpr uint32_t kWaitLimit = 1u << 22;
+__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        if (tc::mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+    }
+    record_device_error(kDevErrTimeout);
+    *abort = 1;
+    return false;
+}
+
 // A whole warp's wait: one answer for all lanes, so that they leave loops together.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort));
+    return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort));
 }
 
 // ---- products issued by a whole warp ----
@@ -208,35 +222,17 @@ template <int D> __device__ __forceinline__ void zero_rows(uint8_t *tile, int fr
     tc::fence_async_smem();
 }
 
-// A warp's 32 rows of D values (thread = row, columns [32 c, 32 c + 32) at a time) to global memory
-// through its own shared memory, so that a row is written in whole 16-byte pieces side by side.
-template <int D> struct RowWriter {
-    static constexpr int CH = D * 2 / 16;
-    uint8_t *smem;
-    __device__ __forceinline__ void put(int lane, int c, const float (&x)[32], float mul) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            uint4 u;
-            u.x = pack_bf16(x[8 * e] * mul, x[8 * e + 1] * mul);
-            u.y = pack_bf16(x[8 * e + 2] * mul, x[8 * e + 3] * mul);
-            u.z = pack_bf16(x[8 * e + 4] * mul, x[8 * e + 5] * mul);
-            u.w = pack_bf16(x[8 * e + 6] * mul, x[8 * e + 7] * mul);
-            const int ch = c * 4 + e;
-            *reinterpret_cast<uint4 *>(smem + lane * (CH * 16) + ((ch ^ (lane & 7)) << 4)) = u;
-        }
+// 16 bf16 numbers to global memory: a whole sector at once where the tensor lies on one.
+__device__ __forceinline__ void store_sector(__nv_bfloat16 *dst, const uint32_t (&u)[8]) {
+    if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                     "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
     }
-    // row r of the warp to dst + r * stride, for r < rows
-    __device__ __forceinline__ void flush(int lane, __nv_bfloat16 *dst, int64_t stride, int rows) {
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int r = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
-            const uint4 u = *reinterpret_cast<const uint4 *>(smem + r * (CH * 16) + ((ch ^ (r & 7)) << 4));
-            if (r < rows) *reinterpret_cast<uint4 *>(dst + r * stride + ch * 8) = u;
-        }
-        __syncwarp();
-    }
-};
+}
 
 // ---- forward ------------------------------------------------------------------------------------
 
@@ -300,16 +296,14 @@ __device__ __forceinline__ TwoTiles item_of(const PromptArgs &a, int pair_heads,
     return w;
 }
 
-// 32 numbers of a thread's row, rounded, to 64 bytes of global memory in two whole sectors at a time.
+// 32 numbers of a thread's row, rounded, to 64 bytes of global memory.
 __device__ __forceinline__ void store32(__nv_bfloat16 *dst, const float (&x)[32], float mul) {
 #pragma unroll
     for (int e = 0; e < 32; e += 16) {
         uint32_t u[8];
 #pragma unroll
         for (int y = 0; y < 8; ++y) u[y] = pack_bf16(x[e + 2 * y] * mul, x[e + 2 * y + 1] * mul);
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + e), "r"(u[0]), "r"(u[1]),
-                     "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-                     : "memory");
+        store_sector(dst + e, u);
     }
 }
 
@@ -423,11 +417,11 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     quit = 0;
-                    if (put_q[i] > 0) tc::mbar_wait(&bars.q_full[i], (put_q[i] - 1) & 1, &quit);
+                    if (put_q[i] > 0) bounded_wait(&bars.q_full[i], (put_q[i] - 1) & 1, &quit);
                 }
                 for (int k = max(0, put - C::kStages); k < put; ++k) {
                     quit = 0;
-                    tc::mbar_wait(&bars.full[k % C::kStages], (k / C::kStages) & 1, &quit);
+                    bounded_wait(&bars.full[k % C::kStages], (k / C::kStages) & 1, &quit);
                 }
             }
         } else if (warp == 18) {

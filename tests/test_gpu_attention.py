@@ -187,6 +187,27 @@ def test_prompt_neighbours_never_mix(dtype, d):
         assert (t[:, 233:] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_outputs_on_sixteen_bytes(dtype):
+    """Outputs and inputs that lie on 16 bytes and no more."""
+    off = 16 // torch.finfo(dtype).bits * 8
+    n = 2 * 70 * 4 * 64
+    q, k, v, _, _ = prompt("two-rows", 4, 4, 64, dtype, seed=87)
+    want = kda.kda_attn_fwd(q, k, v)
+    shifted = []
+    for t in (q, k, v):
+        b = torch.empty(t.numel() + off, dtype=dtype, device="cuda")[off:].view(t.shape)
+        shifted.append(b.copy_(t))
+    out = torch.empty(q.numel() + off, dtype=dtype, device="cuda")[off:].view(q.shape)
+    assert out.data_ptr() % 32 == 16 and n
+    assert torch.equal(kda.kda_attn_fwd(*shifted, out=out), want)
+    kc, vc, table = cache_of([30, 41], 4, 64, 16, dtype, 88)
+    seq = torch.tensor([30, 41], dtype=torch.int32, device="cuda")
+    step = kda.kda_attn_decode_step(q[:, 0], kc, vc, table, seq)
+    o = torch.empty(step.numel() + off, dtype=dtype, device="cuda")[off:].view(step.shape)
+    assert torch.equal(kda.kda_attn_decode_step(shifted[0][:, 0], kc, vc, table, seq, out=o), step)
+
+
 def test_prompt_large_scores():
     """Scores of hundreds: a running maximum that grows tile by tile, and weights that all but vanish."""
     q, k, v, _, _ = prompt("long", 2, 1, 128, BF16, seed=90)
@@ -648,3 +669,26 @@ def test_gradient_in_a_graph_beside_an_eager_one():
     want = torch.autograd.grad(alive, (q, k, v), g)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(16, 4), (6, 6)])
+def test_prompt_more_items_than_sms(hq, hkv, d):
+    """Batches whose tiles outnumber the SMs several times, so that every block works through many."""
+    lens = [700, 33, 1, 0, 390, 128, 517, 256, 64, 900, 300, 129]
+    cu = offsets(lens)
+    q, k, v, g = (make((1, sum(lens), h, d), 830 + i, BF16) for i, h in enumerate((hq, hkv, hkv, hq)))
+    out, lse = kda.kda_attn_fwd(q, k, v, cu, return_lse=True)
+    o, l, tol, ltol = ref.attention(q, k, v, cu)
+    inside(out, o, tol, "out")
+    check_lse(lse, l, ltol)
+    want, tols = ref.attention_grad(q, k, v, g, cu)
+    first = None
+    for _ in range(5):
+        got = kda.kda_attn_bwd(q, k, v, out, lse, g, cu)
+        assert kda.device_error() == 0
+        if first is None:
+            first = got
+            for x, y, t, n in zip(got, want, tols, ("dq", "dk", "dv")):
+                inside(x, y, t, n)
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
