@@ -24,6 +24,8 @@
 // are zeroed in shared memory, since a weight of zero does not hide a NaN.
 #pragma once
 
+#include <limits.h>
+
 #include "attn_prompt_tc.cuh"
 
 namespace kda {
@@ -115,7 +117,11 @@ template <int D> __device__ __forceinline__ uint32_t grad_setup(GradBars &bars, 
 template <int D, int WHICH> struct Ring {
     using C = GradCfg<D>;
     static constexpr int N = WHICH ? C::kSecond : C::kFirst;
-    static __device__ __forceinline__ int stage(int n) { return (WHICH ? C::kFirst : 0) + n % N; }
+    static __device__ __forceinline__ int stage(int n) { return bar(n % N); }
+    // the same by the stage's own number, for those who count it along
+    static __device__ __forceinline__ int bar(int st) { return (WHICH ? C::kFirst : 0) + st; }
+    static __device__ __forceinline__ uint32_t at(int st) { return C::kRing + bar(st) * C::kTileBytes; }
+    static __device__ __forceinline__ int after(int st) { return st + 1 == N ? 0 : st + 1; }
     static __device__ __forceinline__ uint32_t place(int n) { return C::kRing + stage(n) * C::kTileBytes; }
     static __device__ __forceinline__ uint32_t parity(int n) { return (n / N) & 1; }
     // until the stage is free for load n
@@ -159,6 +165,14 @@ __device__ __forceinline__ bool take_item(GradBars &bars, GradItem &w, int r, in
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&bars.item_empty[r & 1]);
     return true;
+}
+// The same for warps that read the item again when its turns are over: it stays until leave_item.
+__device__ __forceinline__ bool see_item(GradBars &bars, int r) {
+    return warp_wait(&bars.item_full[r & 1], (r >> 1) & 1, &bars.abort);
+}
+__device__ __forceinline__ void leave_item(GradBars &bars, int r, int lane) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&bars.item_empty[r & 1]);
 }
 // Blocks take items there and back, so that none has the longest of every round.
 __device__ __forceinline__ int64_t item_index(int r) {
@@ -363,13 +377,13 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
         constexpr uint32_t idG = tc::make_idesc_bf16(kTile, D, false, true);
         const uint32_t leader = elect_lane();
         const uint64_t dK = desc_k(sbase + C::kOwn, 0), dV = desc_k(sbase + C::kOwn + C::kTileBytes, 0);
-        int words = 0;
-        auto scores = [&](int n) {
-            chain_ss<D>(tS(n), dK, desc_k(sbase + R1::place(n), 0), idS, leader);
+        int words = 0, st1 = 0, st2 = 0;   // this turn's stages
+        auto scores = [&](int n, int st) {
+            chain_ss<D>(tS(n), dK, desc_k(sbase + R1::at(st), 0), idS, leader);
             commit_by(&bars.s_full[n & 1], leader);
         };
-        auto products = [&](int n, bool last) {   // dP; the item's own tiles are done with after its last
-            chain_ss<D>(tP, dV, desc_k(sbase + R2::place(n), 0), idS, leader);
+        auto products = [&](int n, int st, bool last) {   // dP; the item's own tiles are done with after its last
+            chain_ss<D>(tP, dV, desc_k(sbase + R2::at(st), 0), idS, leader);
             commit_by(&bars.dp_full[n & 1], leader);
             if (last) commit_by(&bars.own_empty, leader);
         };
@@ -378,29 +392,31 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
             if (total == 0) continue;
             ok = warp_wait(&bars.own_full, own & 1, abort) && warp_wait(&bars.first, own & 1, abort);
             if (!ok) break;
-            scores(base);
-            products(base, total == 1);
-            for (int it = 0; it < total; ++it) {
-                const int n = base + it;
+            scores(base, st1);
+            products(base, st2, total == 1);
+            for (int it = 0; it < total; ++it, ++base) {
                 const bool more = it + 1 < total;
+                const int next1 = R1::after(st1), next2 = R2::after(st2);
+                const uint64_t q = desc_mn(sbase + R1::at(st1), 0), g = desc_mn(sbase + R2::at(st2), 0);
                 if (kAhead && more) {
                     if (!(ok = warp_wait(&bars.q_word, words & 1, abort))) break;
                     ++words;
-                    scores(n + 1);
+                    scores(base + 1, next1);
                 }
-                if (!(ok = wait_turn(bars.a_ready, n, abort))) break;
+                if (!(ok = wait_turn(bars.a_ready, base, abort))) break;
                 tc::tc_fence_after();
-                chain_ts32(tV, tS(n), desc_mn(sbase + R2::place(n), 0), idG, it > 0, leader);
-                if (!kAhead && more) scores(n + 1);
-                commit_by(&bars.empty[R2::stage(n)], leader);
-                if (!(ok = wait_turn(bars.b_ready, n, abort))) break;
+                chain_ts32(tV, tS(base), g, idG, it > 0, leader);
+                if (!kAhead && more) scores(base + 1, next1);
+                commit_by(&bars.empty[R2::bar(st2)], leader);
+                if (!(ok = wait_turn(bars.b_ready, base, abort))) break;
                 tc::tc_fence_after();
-                chain_ts32(tK, tP, desc_mn(sbase + R1::place(n), 0), idG, it > 0, leader);
-                if (more) products(n + 1, it + 2 == total);
-                commit_by(&bars.empty[R1::stage(n)], leader);
+                chain_ts32(tK, tP, q, idG, it > 0, leader);
+                if (more) products(base + 1, next2, it + 2 == total);
+                commit_by(&bars.empty[R1::bar(st1)], leader);
                 if (!more) commit_by(&bars.done, leader);
+                st1 = next1;
+                st2 = next2;
             }
-            base += total;
             ++own;
         }
         if (!ok) {   // no product in flight when the memory is given back
@@ -413,14 +429,17 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
         const uint32_t lanes = tc::tmem_lane_base(warp) + part * 32;
         const float sc = a.scale * kLog2e;
         const float2 sc2 = make_float2(sc, sc);
-        for (int r = 0; ok && (ok = take_item(bars, w, r, lane)) && w.total >= 0; ++r) {
-            const int ahead = w.nk - w.nq;
-            for (int it = 0; it < w.total; ++it, ++base) {
-                const int r0 = (w.start + it % w.per_head) * kTile + part * 32;
+        for (int r = 0; ok && (ok = see_item(bars, r)) && bars.item[r & 1].total >= 0; ++r) {
+            const volatile GradItem &w = bars.item[r & 1];   // read where it is needed, not kept
+            const int total = w.total, begin = w.start * kTile, nq = w.nq;
+            // this row's key is seen from this query on (where masked), and by the warp's rows all
+            const int sees = a.causal ? w.row0 + row - (w.nk - nq) : INT_MIN / 2, all_see = sees + 31 - lane;
+            int r0 = begin;
+            for (int it = 0; it < total; ++it, ++base) {
                 const float *ls = stats + (base & 1) * 2 * kTile + part * 32, *de = ls + kTile;
-                // this row's key is seen by the tile's queries from column `from` on
-                const int from = w.row0 + row - ahead - r0;
-                const bool partly = a.causal && w.row0 + (warp & 3) * 32 + 31 - ahead - r0 > 0;
+                const int from = sees - r0 - part * 32;   // hidden columns before it
+                const bool partly = all_see - r0 - part * 32 > 0;
+                if ((r0 += kTile) >= nq) r0 = begin;
                 ok = warp_wait(&bars.stats[base & 1], (base >> 1) & 1, abort) && wait_turn(bars.s_full, base, abort);
                 if (!ok) break;
                 tc::tc_fence_after();
@@ -472,15 +491,17 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
                 arrive_operand(&bars.b_ready[base & 1], lane);
                 if (lane == 0) tc::mbar_arrive(&bars.stats_read[base & 1]);
             }
-            if (ok && w.total > 0) ok = warp_wait(&bars.done, own++ & 1, abort);
+            if (ok && total > 0) ok = warp_wait(&bars.done, own++ & 1, abort);
             if (!ok) break;
             tc::tc_fence_after();
             // two groups of columns of dV, two of dK
-            const bool is_k = part & 2, there = w.row0 + row < w.nk;
+            const int key = w.row0 + row;
+            const bool is_k = part & 2, there = key < w.nk;
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(is_k ? a.dk : a.dv) +
-                                 ((w.k0 + w.row0 + row) * a.bt.Hkv + w.head) * (int64_t)D + (part & 1) * (D / 2);
+                                 ((w.k0 + key) * a.bt.Hkv + w.head) * (int64_t)D + (part & 1) * (D / 2);
+            leave_item(bars, r, lane);
             store_columns<D / 2>((is_k ? tK : tV) + tc::tmem_lane_base(warp) + (part & 1) * (D / 2), dst,
-                                 is_k ? a.scale : 1.f, w.total == 0, there);
+                                 is_k ? a.scale : 1.f, total == 0, there);
         }
     }
     __syncwarp();
@@ -599,34 +620,37 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
         constexpr uint32_t idG = tc::make_idesc_bf16(kTile, D, false, true);
         const uint32_t leader = elect_lane();
         const uint64_t dQ = desc_k(sbase + C::kOwn, 0), dG = desc_k(sbase + C::kOwn + C::kTileBytes, 0);
-        auto scores = [&](int n, bool last) {   // S and dP; dP alternates between two places
-            const int m = n + own + 1;
-            chain_ss<D>(tS, dQ, desc_k(sbase + R1::place(n), 0), idS, leader);
+        int st1 = 0, st2 = 0;   // stages of this turn's K and of the next load of the second ring
+        auto scores = [&](int n, int st, bool last) {   // S and dP; dP alternates between two places
+            chain_ss<D>(tS, dQ, desc_k(sbase + R1::at(st), 0), idS, leader);
             commit_by(&bars.s_full[n & 1], leader);
-            chain_ss<D>(tP + (n & 1) * kTile, dG, desc_k(sbase + R2::place(m), 0), idS, leader);
+            chain_ss<D>(tP + (n & 1) * kTile, dG, desc_k(sbase + R2::at(st2), 0), idS, leader);
             commit_by(&bars.dp_full[n & 1], leader);
-            commit_by(&bars.empty[R2::stage(m)], leader);
+            commit_by(&bars.empty[R2::bar(st2)], leader);
             if (last) commit_by(&bars.own_empty, leader);
+            st2 = R2::after(st2);
         };
         for (int r = 0; ok && (ok = take_item(bars, w, r, lane)) && w.total >= 0; ++r) {
             const int total = w.total;
             if (total == 0) continue;
             ok = warp_wait(&bars.own_full, own & 1, abort) && warp_wait(&bars.first, own & 1, abort);
             if (!ok) break;
-            scores(base, total == 1);
-            for (int j = 0; j < total; ++j) {
-                const int n = base + j;
+            st2 = R2::after(st2);   // O's
+            scores(base, st1, total == 1);
+            for (int j = 0; j < total; ++j, ++base) {
+                const int next1 = R1::after(st1);
+                const uint64_t k = desc_mn(sbase + R1::at(st1), 0);
                 // the next scores as soon as these have been read
-                if (!(ok = wait_turn(bars.a_ready, n, abort))) break;
+                if (!(ok = wait_turn(bars.a_ready, base, abort))) break;
                 tc::tc_fence_after();
-                if (j + 1 < total) scores(n + 1, j + 2 == total);
-                if (!(ok = wait_turn(bars.b_ready, n, abort))) break;
+                if (j + 1 < total) scores(base + 1, next1, j + 2 == total);
+                if (!(ok = wait_turn(bars.b_ready, base, abort))) break;
                 tc::tc_fence_after();
-                chain_ts32(tQ, tP + (n & 1) * kTile, desc_mn(sbase + R1::place(n), 0), idG, j > 0, leader);
-                commit_by(&bars.empty[R1::stage(n)], leader);
+                chain_ts32(tQ, tP + (base & 1) * kTile, k, idG, j > 0, leader);
+                commit_by(&bars.empty[R1::bar(st1)], leader);
                 if (j + 1 == total) commit_by(&bars.done, leader);
+                st1 = next1;
             }
-            base += total;
             ++own;
         }
         if (!ok) {   // no product in flight when the memory is given back
@@ -640,17 +664,26 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
         const float sc = a.scale * kLog2e;
         const float2 sc2 = make_float2(sc, sc);
         float *parts = reinterpret_cast<float *>(smem + C::kStats);
-        for (int r = 0; ok && (ok = take_item(bars, w, r, lane)) && w.total >= 0; ++r) {
-            const Seq s{w.q0, w.k0, w.nq, w.nk};
-            const int qi = w.row0 + row, first_row = w.row0 + (warp & 3) * 32;
-            const bool there = qi < w.nq;
-            const int seen = there ? keys_seen(s, qi, a.causal) : 0;
-            const int seen_all = first_row + 31 < w.nq ? keys_seen(s, first_row, a.causal) : 0;   // by every row of the warp
-            const int64_t at = there ? stat_at(a.bt, w.q0 + qi, w.head) : 0;
-            float ls = there ? a.lse[at] * kLog2e : -CUDART_INF_F;
-            if (ls != -CUDART_INF_F) ls = -ls;
+        for (int r = 0; ok && (ok = see_item(bars, r)) && bars.item[r & 1].total >= 0; ++r) {
+            const volatile GradItem &w = bars.item[r & 1];   // read where it is needed, not kept
+            const int total = w.total, qi = w.row0 + row;
+            int seen, seen_all;   // keys that this row sees, and every row of the warp
+            bool there;
+            float ls = -CUDART_INF_F;
+            int64_t at = 0;
+            {
+                const Seq s{0, 0, w.nq, w.nk};
+                there = qi < s.nq;
+                seen = there ? keys_seen(s, qi, a.causal) : 0;
+                seen_all = qi - lane + 31 < s.nq ? keys_seen(s, qi - lane, a.causal) : 0;
+                if (there) {
+                    at = stat_at(a.bt, w.q0 + qi, w.head);
+                    ls = a.lse[at] * kLog2e;
+                }
+                if (ls != -CUDART_INF_F) ls = -ls;
+            }
             float de = 0.f;
-            if (w.total > 0) {   // delta = dO . O of this row, a quarter of the channels in each group
+            if (total > 0) {   // delta = dO . O of this row, a quarter of the channels in each group
                 ok = warp_wait(&bars.own_full, own & 1, abort) && R2::wait_full(bars, base + own);
                 if (!ok) break;
                 const uint8_t *g = smem + C::kOwn + C::kTileBytes, *o = smem + R2::place(base + own);
@@ -674,7 +707,7 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
             }
             if (part == 0 && there) a.delta[at] = de;
             const float2 ls2 = make_float2(ls, ls), de2 = make_float2(-de, -de);
-            for (int j = 0; j < w.total; ++j, ++base) {
+            for (int j = 0; j < total; ++j, ++base) {
                 const uint32_t dp = tP + (base & 1) * kTile + lanes;
                 const int limit = seen - j * kTile - part * 32;   // columns at or past it are hidden
                 const bool partly = j * kTile + (part + 1) * 32 > seen_all;
@@ -712,13 +745,14 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                 put_operand(dp, p);
                 arrive_operand(&bars.b_ready[base & 1], lane);
             }
-            if (ok && w.total > 0) ok = warp_wait(&bars.done, own++ & 1, abort);
+            if (ok && total > 0) ok = warp_wait(&bars.done, own++ & 1, abort);
             if (!ok) break;
             tc::tc_fence_after();
-            store_columns<D / 4>(tQ + tc::tmem_lane_base(warp) + part * (D / 4),
-                                 static_cast<__nv_bfloat16 *>(a.dq) + ((w.q0 + qi) * a.bt.Hq + w.head) * (int64_t)D +
-                                     part * (D / 4),
-                                 a.scale, w.total == 0, there);
+            const int to = w.row0 + row;
+            const bool write = to < w.nq;
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.dq) + ((w.q0 + to) * a.bt.Hq + w.head) * (int64_t)D + part * (D / 4);
+            leave_item(bars, r, lane);
+            store_columns<D / 4>(tQ + tc::tmem_lane_base(warp) + part * (D / 4), dst, a.scale, total == 0, write);
         }
     }
     __syncwarp();
