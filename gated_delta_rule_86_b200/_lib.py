@@ -71,8 +71,8 @@ def load() -> ctypes.CDLL:
     lib.kda_chunk_bwd_workspace_size.restype = ctypes.c_int
     i64, f32, size_p = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(ctypes.c_size_t)
     prompt_args = [vp, vp, vp, i64, i64, i64, vp, vp] + [i32] * 8 + [f32, ctypes.c_int]
-    lib.kda_attn_fwd.argtypes = prompt_args + [vp, vp, vp]
-    lib.kda_attn_bwd.argtypes = prompt_args + [vp] * 7 + [ctypes.c_size_t, vp]
+    lib.kda_attn_fwd.argtypes = prompt_args + [vp, vp, vp, vp]
+    lib.kda_attn_bwd.argtypes = prompt_args + [vp] * 8 + [ctypes.c_size_t, vp]
     lib.kda_attn_bwd_workspace_size.argtypes = [i32, i32, i32, size_p]
     lib.kda_kv_append.argtypes = [vp, vp, vp, i64, i64, i64, vp, i32, i32, vp] + [i32] * 6 + \
         [ctypes.c_int, vp, vp, i64, i32, vp, vp, i64, i64, i32, i32, vp, vp, vp]

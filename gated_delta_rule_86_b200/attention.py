@@ -33,24 +33,26 @@ def _native():
 # ---- prompts ------------------------------------------------------------------------------------
 
 
-def kda_attn_fwd(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal=True, scale=None, out=None, return_lse=False):
+def kda_attn_fwd(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal=True, scale=None, out=None, return_lse=False,
+                 return_rest=False):
     """Attention over whole prompts: ``softmax(scale q k^T + mask) v``.
 
     q: [B, Tq, Hq, d]; k, v: [B, Tk, Hkv, d] (bf16 or fp32, d 64 or 128); query head h reads head
     ``h // (Hq // Hkv)``.  cu_seqlens: int32 [N+1] offsets of packed sequences (B == 1), cu_seqlens_k
     those of k and v where they differ.  Causal: query i of a sequence sees keys j <= i + nk - nq; a
     query that sees none gets zeros.  scale: 1 / sqrt(d) by default.  Returns out [B, Tq, Hq, d] in the
-    inputs' dtype, with ``return_lse`` also the fp32 [B, Hq, Tq] logarithms of the softmax sums.  Rows
+    inputs' dtype, with ``return_lse`` also the fp32 [B, Hq, Tq] logarithms of the softmax sums, with
+    ``return_rest`` also what rounding took from a bf16 out (None for fp32), for :func:`kda_attn_bwd`.  Rows
     behind the last packed sequence are not written.
     """
-    return _native().fwd(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale, out, return_lse)
+    return _native().fwd(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale, out, return_lse, return_rest)
 
 
-def kda_attn_bwd(q, k, v, out, lse, d_out, cu_seqlens=None, cu_seqlens_k=None, causal=True, scale=None):
+def kda_attn_bwd(q, k, v, out, lse, d_out, cu_seqlens=None, cu_seqlens_k=None, causal=True, scale=None, out_rest=None):
     """Gradient of :func:`kda_attn_fwd`: ``(dq, dk, dv)`` in the inputs' dtype, from the forward's inputs,
-    its ``out`` and ``lse``, and ``d_out``.  dk and dv are summed over the query heads that share them.
+    its ``out`` and ``lse`` (and ``out_rest``, which takes a third off the error of bf16 dq and dk), and ``d_out``.  dk and dv are summed over the query heads that share them.
     Rows behind the last packed sequence get zeros.  The same call gives the same bits."""
-    return _native().bwd(q, k, v, out, lse, d_out, cu_seqlens, cu_seqlens_k, causal, scale)
+    return _native().bwd(q, k, v, out, lse, d_out, cu_seqlens, cu_seqlens_k, causal, scale, out_rest)
 
 
 def kda_attn(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal=True, scale=None):

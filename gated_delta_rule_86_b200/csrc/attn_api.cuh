@@ -229,14 +229,16 @@ kda_status kda_attn_decode_step(const void *q, int64_t q_stride, const void *k_c
 kda_status kda_attn_fwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
                         int64_t v_stride, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int32_t num_seqs,
                         int32_t B, int32_t Tq, int32_t Tk, int32_t Hq, int32_t Hkv, int32_t d, int32_t causal,
-                        float scale, kda_dtype dtype, void *out, float *lse, void *stream) {
+                        float scale, kda_dtype dtype, void *out, void *out_rest, float *lse, void *stream) {
     using namespace kda::attn;
     PromptArgs a = {};
-    if (!aligned(lse, 4)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(lse, 4) || !aligned(out_rest, 16)) return KDA_ERR_INVALID_ARG;
     const kda_status s = check_prompt(a, q, k, v, q_stride, k_stride, v_stride, cu_seqlens_q, cu_seqlens_k, num_seqs,
                                       B, Tq, Tk, Hq, Hkv, d, causal, scale, dtype, out);
     if (s != KDA_OK) return s;
+    if (out_rest && dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
     a.out = out;
+    a.rest = out_rest;
     a.lse = lse;
     if (Tq == 0) return KDA_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -255,7 +257,7 @@ kda_status kda_attn_bwd_workspace_size(int32_t B, int32_t Tq, int32_t Hq, size_t
 kda_status kda_attn_bwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
                         int64_t v_stride, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int32_t num_seqs,
                         int32_t B, int32_t Tq, int32_t Tk, int32_t Hq, int32_t Hkv, int32_t d, int32_t causal,
-                        float scale, kda_dtype dtype, const void *out, const float *lse, const void *d_out, void *dq,
+                        float scale, kda_dtype dtype, const void *out, const void *out_rest, const float *lse, const void *d_out, void *dq,
                         void *dk, void *dv, void *workspace, size_t workspace_bytes, void *stream) {
     using namespace kda::attn;
     PromptArgs a = {};
@@ -263,12 +265,14 @@ kda_status kda_attn_bwd(const void *q, const void *k, const void *v, int64_t q_s
                                       B, Tq, Tk, Hq, Hkv, d, causal, scale, dtype, out);
     if (s != KDA_OK) return s;
     if ((Tq > 0 && (!lse || !d_out || !dq)) || (Tk > 0 && (!dk || !dv))) return KDA_ERR_INVALID_ARG;
-    const void *ptrs[] = {d_out, dq, dk, dv, workspace};
+    if (out_rest && dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
+    const void *ptrs[] = {out_rest, d_out, dq, dk, dv, workspace};
     for (const void *p : ptrs)
         if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
     if (!aligned(lse, 4)) return KDA_ERR_INVALID_ARG;
     if (Tq > 0 && (!workspace || workspace_bytes < (size_t)B * Tq * Hq * sizeof(float))) return KDA_ERR_INVALID_ARG;
     a.out = const_cast<void *>(out);
+    a.rest = const_cast<void *>(out_rest);
     a.lse = const_cast<float *>(lse);
     a.d_out = d_out;
     a.delta = static_cast<float *>(workspace);

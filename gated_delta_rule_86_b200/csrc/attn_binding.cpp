@@ -168,24 +168,29 @@ Prompt prompt_args(const Tensor &q, const Tensor &k, const Tensor &v, const OptT
     return p;
 }
 
-std::pair<Tensor, Tensor> fwd(const Tensor &q, const Tensor &k, const Tensor &v, const OptTensor &cu,
-                              const OptTensor &cu_k, bool causal, const std::optional<double> &scale,
-                              const OptTensor &out, bool want_lse) {
+// (out, lse, rest); the rest only with the lse, and for bf16 alone
+std::tuple<Tensor, Tensor, Tensor> fwd(const Tensor &q, const Tensor &k, const Tensor &v, const OptTensor &cu,
+                                       const OptTensor &cu_k, bool causal, const std::optional<double> &scale,
+                                       const OptTensor &out, bool want_lse, bool want_rest) {
     const Prompt p = prompt_args(q, k, v, cu, cu_k, causal, scale);
-    Tensor o = take_out(out, q), lse;
+    Tensor o = take_out(out, q), lse, rest;
+    if (want_rest && p.dtype == KDA_BF16) rest = out_like(q);
     if (want_lse) lse = at::empty({p.B, p.Hq, p.Tq}, q.options().dtype(at::kFloat));
     const On on(q);
     check(kda_attn_fwd(ptr(p.q), ptr(p.k), ptr(p.v), p.qs, p.ks, p.vs, int_ptr(p.cu), int_ptr(p.cu_k), p.n, p.B, p.Tq,
-                       p.Tk, p.Hq, p.Hkv, p.d, p.causal, p.scale, p.dtype, ptr(o),
+                       p.Tk, p.Hq, p.Hkv, p.d, p.causal, p.scale, p.dtype, ptr(o), rest.defined() ? ptr(rest) : nullptr,
                        want_lse ? lse.data_ptr<float>() : nullptr, on.stream),
           "kda_attn_fwd");
-    return {o, lse};
+    return {o, lse, rest};
 }
 
 std::tuple<Tensor, Tensor, Tensor> bwd(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &out,
                                        const Tensor &lse, const Tensor &d_out, const OptTensor &cu, const OptTensor &cu_k,
-                                       bool causal, const std::optional<double> &scale) {
+                                       bool causal, const std::optional<double> &scale, const OptTensor &rest) {
     const Prompt p = prompt_args(q, k, v, cu, cu_k, causal, scale);
+    if (rest && rest->sizes() != q.sizes()) bad_value("out_rest must have q's shape");
+    if (rest) same(q, *rest);
+    if (rest && p.dtype != KDA_BF16) bad_type("out_rest goes with bf16 alone");
     if (out.sizes() != q.sizes() || d_out.sizes() != q.sizes() || lse.dim() != 3 || lse.size(0) != p.B ||
         lse.size(1) != p.Hq || lse.size(2) != p.Tq)
         bad_value("out and d_out must have q's shape, and lse [B, Hq, Tq]");
@@ -194,13 +199,15 @@ std::tuple<Tensor, Tensor, Tensor> bwd(const Tensor &q, const Tensor &k, const T
     same(q, out);
     same(q, d_out);
     const Tensor o = tokens(out.contiguous()).first, l = lse.contiguous(), g = tokens(d_out.contiguous()).first;
+    OptTensor re;
+    if (rest) re = tokens(rest->contiguous()).first;
     Tensor dq = out_like(q), dk = out_like(k), dv = out_like(k);
     const On on(q);
     size_t bytes = 0;
     check(kda_attn_bwd_workspace_size(p.B, p.Tq, p.Hq, &bytes), "kda_attn_bwd_workspace_size");
     Tensor ws = at::empty({static_cast<int64_t>(bytes)}, q.options().dtype(at::kByte));
     check(kda_attn_bwd(ptr(p.q), ptr(p.k), ptr(p.v), p.qs, p.ks, p.vs, int_ptr(p.cu), int_ptr(p.cu_k), p.n, p.B, p.Tq,
-                       p.Tk, p.Hq, p.Hkv, p.d, p.causal, p.scale, p.dtype, ptr(o), l.data_ptr<float>(), ptr(g), ptr(dq),
+                       p.Tk, p.Hq, p.Hkv, p.d, p.causal, p.scale, p.dtype, ptr(o), ptr(re), l.data_ptr<float>(), ptr(g), ptr(dq),
                        ptr(dk), ptr(dv), ptr(ws), bytes, on.stream),
           "kda_attn_bwd");
     return {dq, dk, dv};
@@ -210,8 +217,8 @@ std::tuple<Tensor, Tensor, Tensor> bwd(const Tensor &q, const Tensor &k, const T
 struct Attention : torch::autograd::Function<Attention> {
     static Tensor forward(torch::autograd::AutogradContext *ctx, const Tensor &q, const Tensor &k, const Tensor &v,
                           const OptTensor &cu, const OptTensor &cu_k, bool causal, const std::optional<double> &scale) {
-        auto [out, lse] = fwd(q, k, v, cu, cu_k, causal, scale, std::nullopt, true);
-        ctx->save_for_backward({q, k, v, out, lse, cu.value_or(Tensor()), cu_k.value_or(Tensor())});
+        auto [out, lse, rest] = fwd(q, k, v, cu, cu_k, causal, scale, std::nullopt, true, true);
+        ctx->save_for_backward({q, k, v, out, lse, cu.value_or(Tensor()), cu_k.value_or(Tensor()), rest});
         ctx->saved_data["causal"] = causal;
         ctx->saved_data["scale"] = scale ? c10::IValue(*scale) : c10::IValue();
         return out;
@@ -227,7 +234,7 @@ struct Attention : torch::autograd::Function<Attention> {
         if (grads[0].defined())
             std::tie(dq, dk, dv) =
                 bwd(s[0], s[1], s[2], s[3], s[4], grads[0], opt(s[5]), opt(s[6]), ctx->saved_data["causal"].toBool(),
-                    scale.isNone() ? std::optional<double>() : std::optional<double>(scale.toDouble()));
+                    scale.isNone() ? std::optional<double>() : std::optional<double>(scale.toDouble()), opt(s[7]));
         return {dq, dk, dv, Tensor(), Tensor(), Tensor(), Tensor()};
     }
 };
@@ -365,10 +372,14 @@ PYBIND11_MODULE(_attention, m) {
         }
     });
     m.def("fwd", [](const Tensor &q, const Tensor &k, const Tensor &v, const OptTensor &cu, const OptTensor &cu_k, bool causal,
-                    std::optional<double> scale, const OptTensor &out, bool return_lse) -> py::object {
-        auto [o, lse] = fwd(q, k, v, cu, cu_k, causal, scale, out, return_lse);
-        if (return_lse) return py::make_tuple(o, lse);
-        return py::cast(o);
+                    std::optional<double> scale, const OptTensor &out, bool return_lse, bool return_rest) -> py::object {
+        auto [o, lse, rest] = fwd(q, k, v, cu, cu_k, causal, scale, out, return_lse, return_rest);
+        if (!return_lse && !return_rest) return py::cast(o);
+        py::list all;
+        all.append(o);
+        if (return_lse) all.append(lse);
+        if (return_rest) all.append(rest.defined() ? py::cast(rest) : py::none());
+        return py::tuple(all);
     });
     m.def("bwd", &bwd);
     m.def("attn", [](const Tensor &q, const Tensor &k, const Tensor &v, const OptTensor &cu, const OptTensor &cu_k, bool causal,

@@ -683,7 +683,17 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                 if (ls != -CUDART_INF_F) ls = -ls;
             }
             float de = 0.f;
-            if (total > 0) {   // delta = dO . O of this row, a quarter of the channels in each group
+            if (total > 0) {
+                // delta = dO . O of this row, a quarter of the channels in each group, with O as exact as the
+                // forward gives it: a delta from the rounded O alone errs by as much as rounding dS does
+                uint4 rest[D / 32];
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y)
+                    rest[y] = a.rest && there ? __ldg(reinterpret_cast<const uint4 *>(
+                                                          static_cast<const __nv_bfloat16 *>(a.rest) +
+                                                          ((w.q0 + qi) * a.bt.Hq + w.head) * (int64_t)D) +
+                                                      part * (D / 32) + y)
+                                              : make_uint4(0, 0, 0, 0);
                 ok = warp_wait(&bars.own_full, own & 1, abort) && R2::wait_full(bars, base + own);
                 if (!ok) break;
                 const uint8_t *g = smem + C::kOwn + C::kTileBytes, *o = smem + R2::place(base + own);
@@ -692,11 +702,13 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                     const int c = part * (D / 32) + y;
                     const uint32_t off = (c >> 3) * (kTile * 128) + tc::sw128(row, c & 7);
                     const uint4 u = *reinterpret_cast<const uint4 *>(g + off), v = *reinterpret_cast<const uint4 *>(o + off);
-                    const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+                    const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w},
+                                   rs[4] = {rest[y].x, rest[y].y, rest[y].z, rest[y].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        de = fmaf(__uint_as_float(us[e] << 16), __uint_as_float(vs[e] << 16), de);
-                        de = fmaf(__uint_as_float(us[e] & 0xffff0000u), __uint_as_float(vs[e] & 0xffff0000u), de);
+                        de = fmaf(__uint_as_float(us[e] << 16), __uint_as_float(vs[e] << 16) + __uint_as_float(rs[e] << 16), de);
+                        de = fmaf(__uint_as_float(us[e] & 0xffff0000u),
+                                  __uint_as_float(vs[e] & 0xffff0000u) + __uint_as_float(rs[e] & 0xffff0000u), de);
                     }
                 }
                 parts[part * kTile + row] = de;

@@ -31,6 +31,7 @@ struct PromptArgs {
     bool causal;
     float scale;
     void *out;
+    void *rest;                             // bf16: what rounding took from out, or null
     float *lse;                             // [B][Hq][Tq]
     // gradient only
     const void *d_out;

@@ -296,14 +296,22 @@ __device__ __forceinline__ TwoTiles item_of(const PromptArgs &a, int pair_heads,
     return w;
 }
 
-// 32 numbers of a thread's row, rounded, to 64 bytes of global memory.
-__device__ __forceinline__ void store32(__nv_bfloat16 *dst, const float (&x)[32], float mul) {
+// 32 numbers of a thread's row, rounded, to 64 bytes of global memory, and what the rounding took from them,
+// rounded in its turn (together they are good to 2^-17), where that is asked for.
+__device__ __forceinline__ void store32(__nv_bfloat16 *dst, __nv_bfloat16 *rest, const float (&x)[32], float mul) {
 #pragma unroll
     for (int e = 0; e < 32; e += 16) {
         uint32_t u[8];
 #pragma unroll
         for (int y = 0; y < 8; ++y) u[y] = pack_bf16(x[e + 2 * y] * mul, x[e + 2 * y + 1] * mul);
         store_sector(dst + e, u);
+        if (rest) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+                u[y] = pack_bf16(x[e + 2 * y] * mul - __uint_as_float(u[y] << 16),
+                                 x[e + 2 * y + 1] * mul - __uint_as_float(u[y] & 0xffff0000u));
+            store_sector(rest + e, u);
+        }
     }
 }
 
@@ -645,9 +653,11 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = 0.f;
             }
-            if (there)
-                store32(static_cast<__nv_bfloat16 *>(a.out) + (at * a.bt.Hq + head) * (int64_t)D + half * (D / 2) + c * 32, o,
-                        inv);
+            if (there) {
+                const int64_t to = (at * a.bt.Hq + head) * (int64_t)D + half * (D / 2) + c * 32;
+                store32(static_cast<__nv_bfloat16 *>(a.out) + to,
+                        a.rest ? static_cast<__nv_bfloat16 *>(a.rest) + to : nullptr, o, inv);
+            }
         }
         if (a.lse && half == 0 && there) a.lse[stat_at(a.bt, at, head)] = l == 0.f ? -CUDART_INF_F : m * a.scale + logf(l);
         had ^= blocks > 0;

@@ -345,6 +345,8 @@ kda_status kda_chunk_bwd_workspace_size(int32_t N, int32_t H, int64_t total_toke
  *                   query that sees none gets out = 0, lse = -inf.
  *   scale         : finite and positive.
  *   out           : [B, Tq, Hq, d];  lse : fp32 [B, Hq, Tq], or NULL.
+ *   out_rest      : NULL, or bf16 [B, Tq, Hq, d] (bf16 calls only): what rounding
+ *                   took from out, for a more exact gradient.
  * A sequence never sees another's keys, whatever they hold (NaN included).
  * Inside a sequence, keys and values that the causal mask hides must be finite
  * for bf16: a hidden value enters the tensor cores' sums with weight zero.
@@ -352,8 +354,8 @@ kda_status kda_chunk_bwd_workspace_size(int32_t N, int32_t H, int64_t total_toke
 kda_status kda_attn_fwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
                         int64_t v_stride, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
                         int32_t num_seqs, int32_t B, int32_t Tq, int32_t Tk, int32_t Hq, int32_t Hkv,
-                        int32_t d, int32_t causal, float scale, kda_dtype dtype, void *out, float *lse,
-                        void *stream);
+                        int32_t d, int32_t causal, float scale, kda_dtype dtype, void *out,
+                        void *out_rest, float *lse, void *stream);
 
 /*
  * kda_attn_bwd -- gradient of kda_attn_fwd.
@@ -361,7 +363,8 @@ kda_status kda_attn_fwd(const void *q, const void *k, const void *v, int64_t q_s
  *     P = exp(scale Q K^T - lse),  delta = rowsum(dO o O),  dS = P o (dO V^T - delta),
  *     dV = P^T dO,   dK = scale dS^T Q,   dQ = scale dS K
  * with dK and dV summed over the query heads of a group.  Takes the forward's
- * inputs, its out and lse, and d_out [B, Tq, Hq, d] (dense); writes dq [B, Tq,
+ * inputs, its out and lse, out_rest (or NULL: delta is then formed from the
+ * rounded out, and dQ and dK err by up to a third more), and d_out [B, Tq, Hq, d] (dense); writes dq [B, Tq,
  * Hq, d], dk and dv [B, Tk, Hkv, d] in the inputs' type.  Rows behind the last
  * packed sequence get zero gradients.  The order of every sum is fixed: the
  * same call gives the same bits.  workspace: kda_attn_bwd_workspace_size bytes.
@@ -370,7 +373,7 @@ kda_status kda_attn_bwd(const void *q, const void *k, const void *v, int64_t q_s
                         int64_t v_stride, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
                         int32_t num_seqs, int32_t B, int32_t Tq, int32_t Tk, int32_t Hq, int32_t Hkv,
                         int32_t d, int32_t causal, float scale, kda_dtype dtype, const void *out,
-                        const float *lse, const void *d_out, void *dq, void *dk, void *dv,
+                        const void *out_rest, const float *lse, const void *d_out, void *dq, void *dk, void *dv,
                         void *workspace, size_t workspace_bytes, void *stream);
 kda_status kda_attn_bwd_workspace_size(int32_t B, int32_t Tq, int32_t Hq, size_t *bytes);
 

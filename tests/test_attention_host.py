@@ -23,14 +23,14 @@ def lib():
 
 
 def fwd(lib, q=F, k=F, v=F, qs=0, ks=0, vs=0, cu=None, cuk=None, n=0, B=1, Tq=8, Tk=8, Hq=4, Hkv=2, d=64, scale=0.1,
-        dt=B16, out=F, lse=None):
-    return lib.kda_attn_fwd(q, k, v, qs, ks, vs, cu, cuk, n, B, Tq, Tk, Hq, Hkv, d, 1, scale, dt, out, lse, None)
+        dt=B16, out=F, rest=None, lse=None):
+    return lib.kda_attn_fwd(q, k, v, qs, ks, vs, cu, cuk, n, B, Tq, Tk, Hq, Hkv, d, 1, scale, dt, out, rest, lse, None)
 
 
-def bwd(lib, Tq=8, Tk=8, out=F, lse=F, g=F, dq=F, dk=F, dv=F, ws=F, size=1 << 20, **kw):
+def bwd(lib, Tq=8, Tk=8, out=F, rest=None, lse=F, g=F, dq=F, dk=F, dv=F, ws=F, size=1 << 20, **kw):
     a = dict(Hq=4, Hkv=2, d=64, scale=0.1, dt=B16) | kw
     return lib.kda_attn_bwd(F, F, F, 0, 0, 0, None, None, 0, 1, Tq, Tk, a["Hq"], a["Hkv"], a["d"], 1, a["scale"], a["dt"],
-                            out, lse, g, dq, dk, dv, ws, size, None)
+                            out, rest, lse, g, dq, dk, dv, ws, size, None)
 
 
 def append(lib, q=F, k=F, v=F, qs=0, ks=0, vs=0, freq=F, rot=64, cu=None, n=0, B=1, T=1, Hq=4, Hkv=2, d=64, dt=B16,
@@ -52,7 +52,7 @@ BAD_HEADS = [(dict(Hq=3), E), (dict(Hkv=0), E), (dict(d=0), E), (dict(dt=9), E),
     (dict(q=None), E), (dict(k=None), E), (dict(out=None), E), (dict(v=ODD), E), (dict(B=0), E), (dict(Tq=-1), E),
     (dict(scale=0.0), E), (dict(scale=-1.0), E), (dict(scale=float("nan")), E), (dict(scale=float("inf")), E),
     (dict(qs=100), E), (dict(qs=260), E), (dict(ks=129), E), (dict(cuk=F), E), (dict(cu=F, n=0), E),
-    (dict(cu=F, n=2, B=2), E), (dict(cu=F, n=2, Tk=9), E), (dict(cu=F + 2, n=2), E), (dict(lse=F + 2), E),
+    (dict(cu=F, n=2, B=2), E), (dict(cu=F, n=2, Tk=9), E), (dict(cu=F + 2, n=2), E), (dict(lse=F + 2), E), (dict(rest=ODD), E), (dict(rest=F, dt=F32), E),
     (dict(B=1 << 20, Tq=1 << 12, Tk=1 << 12), U)])
 def test_forward_refuses(lib, kw, want):
     assert fwd(lib, **kw) == want
@@ -60,7 +60,7 @@ def test_forward_refuses(lib, kw, want):
 
 @pytest.mark.parametrize("kw,want", BAD_HEADS + [
     (dict(out=None), E), (dict(lse=None), E), (dict(g=None), E), (dict(dq=None), E), (dict(dk=None), E), (dict(dv=None), E),
-    (dict(ws=None), E), (dict(size=8 * 4 * 4 - 1), E), (dict(dq=ODD), E), (dict(g=ODD), E), (dict(scale=0.0), E)])
+    (dict(ws=None), E), (dict(size=8 * 4 * 4 - 1), E), (dict(dq=ODD), E), (dict(g=ODD), E), (dict(rest=ODD), E), (dict(rest=F, dt=F32), E), (dict(scale=0.0), E)])
 def test_gradient_refuses(lib, kw, want):
     assert bwd(lib, **kw) == want
 
