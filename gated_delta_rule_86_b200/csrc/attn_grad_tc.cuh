@@ -210,15 +210,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return d;
 }
 
-// Gradients of rows behind the last packed sequence: zero.  Normally there are none; every block takes its share.
-template <int D> __device__ __forceinline__ void zero_behind(__nv_bfloat16 *g, const int32_t *cu, int n, int T, int heads) {
-    if (cu == nullptr) return;
-    const int from = min(max(__ldg(cu + n), 0), T);
-    const int64_t pieces = (int64_t)(T - from) * heads * (D / 8);
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * blockDim.x)
-        reinterpret_cast<uint4 *>(g + (int64_t)from * heads * D)[i] = make_uint4(0, 0, 0, 0);
-}
-
 // N columns of a thread's row of an accumulator to global memory.
 template <int N> __device__ __forceinline__ void store_columns(uint32_t taddr, __nv_bfloat16 *dst, float mul, bool zero, bool there) {
 #pragma unroll
@@ -255,8 +246,8 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
     const uint32_t tmem = grad_setup<D>(bars, {1, kAhead ? 16 : 17, 17, 19});
     if (tid == 32) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&maps.g);
     wait_for_previous();
-    zero_behind<D>(static_cast<__nv_bfloat16 *>(a.dk), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv);
-    zero_behind<D>(static_cast<__nv_bfloat16 *>(a.dv), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv);
+    zero_behind(static_cast<__nv_bfloat16 *>(a.dk), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
+    zero_behind(static_cast<__nv_bfloat16 *>(a.dv), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
 
     volatile int *abort = &bars.abort;
     const int group = a.bt.Hq / a.bt.Hkv;
@@ -530,7 +521,7 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
     const uint32_t tmem = grad_setup<D>(bars, {2, 17, 16, 18});
     if (tid == 32) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&maps.g), prefetch_map(&maps.o);
     wait_for_previous();
-    zero_behind<D>(static_cast<__nv_bfloat16 *>(a.dq), a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq);
+    zero_behind(static_cast<__nv_bfloat16 *>(a.dq), a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq * D);
 
     volatile int *abort = &bars.abort;
     const uint32_t tS = tmem, tP = tmem + kTile, tQ = tmem + 3 * kTile;

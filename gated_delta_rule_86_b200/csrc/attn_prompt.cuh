@@ -13,9 +13,10 @@
 //
 // fp32 inputs ask for fp32 accuracy, which the tensor cores' operands do not give; these kernels are
 // bound by the FMA units and, for small batches, by the latency of a tile.  A block has ROWS rows of one
-// head and walks tiles of 64 of the other side; thread (ty, tx) holds 4 x 4 scores, rows
-// 4 ty .. 4 ty + 3, so a row's 16 threads lie in one half of a warp and its maximum and sum are four
-// shuffles.  The next tile is on its way (cp.async) while one is worked on.
+// head and walks tiles of 64 of the other side; thread (ty, tx) holds RPT x 4 scores, rows
+// RPT ty and on, so a row's 16 threads lie in one half of a warp and its maximum and sum are four shuffles.
+// Large batches have 64 rows a block and 4 a thread (16 products for 8 loads from shared memory), small
+// ones 16 and 2 (a turn is done sooner).  The next tile is on its way (cp.async) while one is worked on.
 #pragma once
 
 #include "attn_append.cuh"
@@ -76,32 +77,32 @@ __device__ __forceinline__ void stage_rows(float *dst, const float *src, int64_t
     }
 }
 
-// acc[i][j] += A[4 ty + i] . B[tx + 16 j] over D channels (pitch D + 4)
-template <int D> __device__ __forceinline__ void dot_rows(float (&acc)[4][4], const float *A, const float *B, int ty,
-                                                          int tx) {
+// acc[i][j] += A[RPT ty + i] . B[tx + 16 j] over D channels (pitch D + 4)
+template <int D, int RPT>
+__device__ __forceinline__ void dot_rows(float (&acc)[RPT][4], const float *A, const float *B, int ty, int tx) {
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
-        float4 a[4], b[4];
+        float4 a[RPT], b[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(A + (4 * ty + i) * (D + 4) + c);
+        for (int i = 0; i < RPT; ++i) a[i] = *reinterpret_cast<const float4 *>(A + (RPT * ty + i) * (D + 4) + c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * (D + 4) + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RPT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 acc[i][j] += a[i].x * b[j].x + a[i].y * b[j].y + a[i].z * b[j].z + a[i].w * b[j].w;
     }
 }
 
-// acc[i][c] += sum_t W[4 ty + i][t] X[t][channel c of tx]  (W pitch 68, X pitch D + 4)
-template <int D> __device__ __forceinline__ void weigh_rows(float (&acc)[4][D / 16], const float *W, const float *X,
-                                                            int ty, int tx) {
+// acc[i][c] += sum_t W[RPT ty + i][t] X[t][channel c of tx]  (W pitch 68, X pitch D + 4)
+template <int D, int RPT>
+__device__ __forceinline__ void weigh_rows(float (&acc)[RPT][D / 16], const float *W, const float *X, int ty, int tx) {
 #pragma unroll 2
     for (int t = 0; t < kPT; t += 4) {
-        float4 w[4];
+        float4 w[RPT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4 *>(W + (4 * ty + i) * 68 + t);
+        for (int i = 0; i < RPT; ++i) w[i] = *reinterpret_cast<const float4 *>(W + (RPT * ty + i) * 68 + t);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             float x[D / 16];
@@ -111,7 +112,7 @@ template <int D> __device__ __forceinline__ void weigh_rows(float (&acc)[4][D / 
                 x[c] = f.x, x[c + 1] = f.y, x[c + 2] = f.z, x[c + 3] = f.w;
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < RPT; ++i) {
                 const float wi = u == 0 ? w[i].x : u == 1 ? w[i].y : u == 2 ? w[i].z : w[i].w;
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) acc[i][c] += wi * x[c];
@@ -128,19 +129,24 @@ template <int D> __device__ __forceinline__ void write_row(float *dst, const flo
             make_float4(acc[c] * mul, acc[c + 1] * mul, acc[c + 2] * mul, acc[c + 3] * mul);
 }
 
-// A thread's 4 x 4 weights into shared memory; a row's come from the half warp that reads them.
-__device__ __forceinline__ void put_weights(float *sp, const float (&x)[4][4], int ty, int tx) {
+// A thread's weights into shared memory; a row's come from the half warp that reads them.
+template <int RPT> __device__ __forceinline__ void put_weights(float *sp, const float (&x)[RPT][4], int ty, int tx) {
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RPT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sp[(4 * ty + i) * 68 + tx + 16 * j] = x[i][j];
+        for (int j = 0; j < 4; ++j) sp[(RPT * ty + i) * 68 + tx + 16 * j] = x[i][j];
     __syncwarp();
 }
 
-template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_prompt_kernel(const PromptArgs a) {
+template <int ROWS> struct RowsCfg {
+    static constexpr int kPer = ROWS == 64 ? 4 : 2;        // rows of a thread
+    static constexpr int kThreads = ROWS / kPer * 16;
+};
+
+template <int D, int ROWS> __global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_prompt_kernel(const PromptArgs a) {
     using C = PromptCfg<D>;
-    constexpr int THREADS = ROWS * 4;
+    constexpr int THREADS = RowsCfg<ROWS>::kThreads, RPT = RowsCfg<ROWS>::kPer;
     extern __shared__ __align__(16) float sm[];
     float *sq = sm, *ring = sq + ROWS * C::kPitch, *sp = ring + 4 * C::kTileF;
     int *scratch = reinterpret_cast<int *>(sp + ROWS * 68 + 4 * kPT);
@@ -164,9 +170,9 @@ template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_prom
     load(0, 0);
 
     const float sc = a.scale * kLog2e;
-    float m[4], l[4], o[4][D / 16];
+    float m[RPT], l[RPT], o[RPT][D / 16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RPT; ++i) {
         m[i] = -CUDART_INF_F;
         l[i] = 0.f;
 #pragma unroll
@@ -177,11 +183,11 @@ template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_prom
         copies_wait();
         __syncthreads();
         load(c0 + kPT, at ^ 1);
-        float x[4][4] = {};
-        dot_rows<D>(x, sq, ring + 2 * at * C::kTileF, ty, tx);
+        float x[RPT][4] = {};
+        dot_rows<D, RPT>(x, sq, ring + 2 * at * C::kTileF, ty, tx);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int seen = keys_seen(s, r0 + 4 * ty + i, a.causal) - c0;
+        for (int i = 0; i < RPT; ++i) {
+            const int seen = keys_seen(s, r0 + RPT * ty + i, a.causal) - c0;
             float top = -CUDART_INF_F;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -203,12 +209,12 @@ template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_prom
             for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
         }
         put_weights(sp, x, ty, tx);
-        weigh_rows<D>(o, sp, ring + (2 * at + 1) * C::kTileF, ty, tx);
+        weigh_rows<D, RPT>(o, sp, ring + (2 * at + 1) * C::kTileF, ty, tx);
     }
     copies_wait();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 4 * ty + i;
+    for (int i = 0; i < RPT; ++i) {
+        const int r = r0 + RPT * ty + i;
         float sum = l[i];
 #pragma unroll
         for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -221,48 +227,17 @@ template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_prom
     }
 }
 
-// delta_i = dO_i . O_i, one warp per (query, head).  Rows behind the last sequence get zero gradients
-// here: no other kernel visits them.
-template <int D> __global__ void __launch_bounds__(256) attn_delta_kernel(const PromptArgs a) {
-    using T = float;
-    constexpr int VE = Vec16<T>::N;
-    constexpr int LANES = D / VE;   // lanes of a row
-    const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
-    const int lane = threadIdx.x % LANES;
-    const int64_t rows_q = (int64_t)(a.bt.cu_q ? 1 : a.bt.n) * a.bt.Tq, rows_k = (int64_t)(a.bt.cu_q ? 1 : a.bt.n) * a.bt.Tk;
-    const int64_t nq = rows_q * a.bt.Hq, nk = rows_k * a.bt.Hkv;
-    float dot = 0.f;
-    if (item < nq) {
-        const int64_t row = item / a.bt.Hq;
-        const Vec16<T> x = load16(static_cast<const T *>(a.d_out) + item * D + lane * VE);
-        const Vec16<T> y = load16(static_cast<const T *>(a.out) + item * D + lane * VE);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) dot += to_f32(x.x[e]) * to_f32(y.x[e]);
-        if (a.bt.cu_q && row >= __ldg(a.bt.cu_q + a.bt.n)) {
-            Vec16<T> z = {};
-            store16(static_cast<T *>(a.dq) + item * D + lane * VE, z);
-        }
-    }
-#pragma unroll
-    for (int d = LANES / 2; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-    if (item < nq && lane == 0) a.delta[stat_at(a.bt, item / a.bt.Hq, (int)(item % a.bt.Hq))] = dot;
-    if (a.bt.cu_k && item < nk && item / a.bt.Hkv >= __ldg(a.bt.cu_k + a.bt.n)) {
-        Vec16<T> z = {};
-        store16(static_cast<T *>(a.dk) + item * D + lane * VE, z);
-        store16(static_cast<T *>(a.dv) + item * D + lane * VE, z);
-    }
-}
-
-// P and dS of one 64 x 64 tile: x (scores, log2 units) and y (dP) in, both out in place.
+// P and dS of a tile: x (scores, log2 units) and y (dP) in, both out in place.
 // `transposed`: rows of the thread's block are keys, columns queries.
-__device__ __forceinline__ void grad_scores(float (&x)[4][4], float (&y)[4][4], const Seq &s, const float *lse2,
+template <int RPT>
+__device__ __forceinline__ void grad_scores(float (&x)[RPT][4], float (&y)[RPT][4], const Seq &s, const float *lse2,
                                             const float *delta, int r0, int c0, int ty, int tx, bool causal,
                                             bool transposed) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RPT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int qi = transposed ? tx + 16 * j : 4 * ty + i, kj = transposed ? 4 * ty + i : tx + 16 * j;
+            const int qi = transposed ? tx + 16 * j : RPT * ty + i, kj = transposed ? RPT * ty + i : tx + 16 * j;
             const bool seen = r0 + qi < s.nq && c0 + kj < keys_seen(s, r0 + qi, causal);
             const float p = seen ? exp2f(x[i][j] - lse2[qi]) : 0.f;
             x[i][j] = p;
@@ -287,15 +262,28 @@ __device__ __forceinline__ void stage_stats(float *lse2, float *delta, const Pro
     }
 }
 
+// Gradients of rows behind the last packed sequence: zero.  Normally there are none; every block takes its
+// share, in 16-byte pieces (`row` elements each).
+template <typename T> __device__ __forceinline__ void zero_behind(T *g, const int32_t *cu, int n, int T_, int row) {
+    if (cu == nullptr) return;
+    const int from = min(max(__ldg(cu + n), 0), T_);
+    const int64_t pieces = (int64_t)(T_ - from) * row * (int)sizeof(T) / 16;
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, blocks = (int64_t)gridDim.x * gridDim.y;
+    for (int64_t i = block * blockDim.x + threadIdx.x; i < pieces; i += blocks * blockDim.x)
+        reinterpret_cast<uint4 *>(g + (int64_t)from * row)[i] = make_uint4(0, 0, 0, 0);
+}
+
 // dK and dV of ROWS keys of one head of the cache, over all query heads of its group.
-template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_grad_kv_kernel(const PromptArgs a) {
+template <int D, int ROWS> __global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_grad_kv_kernel(const PromptArgs a) {
     using C = PromptCfg<D>;
-    constexpr int THREADS = ROWS * 4;
+    constexpr int THREADS = RowsCfg<ROWS>::kThreads, RPT = RowsCfg<ROWS>::kPer;
     extern __shared__ __align__(16) float sm[];
     float *sk = sm, *sv = sk + ROWS * C::kPitch, *ring = sv + ROWS * C::kPitch, *sp = ring + 4 * C::kTileF,
           *stats = sp + ROWS * 68;   // lse and delta of two tiles
     int *scratch = reinterpret_cast<int *>(stats + 4 * kPT);
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, hk = blockIdx.y;
+    zero_behind(static_cast<float *>(a.dk), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
+    zero_behind(static_cast<float *>(a.dv), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
     int n, t;
     if (!find_tile(a.bt.cu_k, a.bt.n, a.bt.Tk, ROWS, blockIdx.x, scratch, n, t)) return;
     const Seq s = seq_of(a.bt, n);
@@ -322,30 +310,30 @@ template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_grad
                                  s.nk);
     load(0, 0);
     const float sc = a.scale * kLog2e;
-    float gk[4][D / 16] = {}, gv[4][D / 16] = {};
+    float gk[RPT][D / 16] = {}, gv[RPT][D / 16] = {};
     for (int it = 0; it < total; ++it) {
         const int at = it & 1, r0 = (start + it % per_head) * kPT;
         const float *sq = ring + 2 * at * C::kTileF, *sg = sq + C::kTileF;
         copies_wait();
         __syncthreads();
         load(it + 1, at ^ 1);
-        float x[4][4] = {}, y[4][4] = {};
-        dot_rows<D>(x, sk, sq, ty, tx);
-        dot_rows<D>(y, sv, sg, ty, tx);
+        float x[RPT][4] = {}, y[RPT][4] = {};
+        dot_rows<D, RPT>(x, sk, sq, ty, tx);
+        dot_rows<D, RPT>(y, sv, sg, ty, tx);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RPT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[i][j] *= sc;
         grad_scores(x, y, s, stats + 2 * at * kPT, stats + (2 * at + 1) * kPT, r0, c0, ty, tx, a.causal, true);
         put_weights(sp, x, ty, tx);
-        weigh_rows<D>(gv, sp, sg, ty, tx);
+        weigh_rows<D, RPT>(gv, sp, sg, ty, tx);
         put_weights(sp, y, ty, tx);
-        weigh_rows<D>(gk, sp, sq, ty, tx);
+        weigh_rows<D, RPT>(gk, sp, sq, ty, tx);
     }
     copies_wait();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = c0 + 4 * ty + i;
+    for (int i = 0; i < RPT; ++i) {
+        const int r = c0 + RPT * ty + i;
         if (r >= s.nk) continue;
         const int64_t to = ((s.k0 + r) * a.bt.Hkv + hk) * D;
         write_row<D>(static_cast<float *>(a.dk) + to, gk[i], tx, a.scale);
@@ -353,15 +341,16 @@ template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_grad
     }
 }
 
-// dQ of ROWS queries of one head.
-template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_grad_q_kernel(const PromptArgs a) {
+// dQ of ROWS queries of one head; and their delta = dO . O, which the keys' kernel reads after this one.
+template <int D, int ROWS> __global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_grad_q_kernel(const PromptArgs a) {
     using C = PromptCfg<D>;
-    constexpr int THREADS = ROWS * 4;
+    constexpr int THREADS = RowsCfg<ROWS>::kThreads, RPT = RowsCfg<ROWS>::kPer;
     extern __shared__ __align__(16) float sm[];
     float *sq = sm, *sg = sq + ROWS * C::kPitch, *ring = sg + ROWS * C::kPitch, *sp = ring + 4 * C::kTileF,
           *stats = sp + ROWS * 68;
     int *scratch = reinterpret_cast<int *>(stats + 4 * kPT);
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, h = blockIdx.y;
+    zero_behind(static_cast<float *>(a.dq), a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq * D);
     int n, t;
     if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, ROWS, gridDim.x - 1 - blockIdx.x, scratch, n, t)) return;
     const Seq s = seq_of(a.bt, n);
@@ -381,30 +370,56 @@ template <int D, int ROWS> __global__ void __launch_bounds__(ROWS * 4) attn_grad
     stage_rows<D, ROWS, THREADS>(sg, static_cast<const float *>(a.d_out) + (s.q0 * a.bt.Hq + h) * (int64_t)D,
                                  (int64_t)a.bt.Hq * D, r0, s.nq);
     load(0, 0);
-    stage_stats<ROWS, THREADS>(stats, stats + kPT, a, s, r0, h);
+    copies_wait();
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int r = RPT * ty + i;
+        const bool there = r0 + r < s.nq;
+        const float *o = static_cast<const float *>(a.out) + ((s.q0 + r0 + r) * a.bt.Hq + h) * (int64_t)D;
+        float dot = 0.f;
+#pragma unroll
+        for (int c = tx * 4; c < D; c += 64) {
+            const float4 x = there ? *reinterpret_cast<const float4 *>(o + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 y = *reinterpret_cast<const float4 *>(sg + r * C::kPitch + c);
+            dot += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+        }
+#pragma unroll
+        for (int d = 8; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+        if (tx == 0) {
+            float lse = 0.f;
+            if (there) {
+                const int64_t to = stat_at(a.bt, s.q0 + r0 + r, h);
+                a.delta[to] = dot;
+                lse = a.lse[to] * kLog2e;
+            }
+            stats[r] = lse == -CUDART_INF_F ? 0.f : lse;
+            stats[kPT + r] = dot;
+        }
+    }
     const float sc = a.scale * kLog2e;
-    float gq[4][D / 16] = {};
+    float gq[RPT][D / 16] = {};
     int at = 0;
     for (int c0 = 0; c0 < end; c0 += kPT, at ^= 1) {
         copies_wait();
         __syncthreads();
         load(c0 + kPT, at ^ 1);
         const float *sk = ring + 2 * at * C::kTileF, *sv = sk + C::kTileF;
-        float x[4][4] = {}, y[4][4] = {};
-        dot_rows<D>(x, sq, sk, ty, tx);
-        dot_rows<D>(y, sg, sv, ty, tx);
+        float x[RPT][4] = {}, y[RPT][4] = {};
+        dot_rows<D, RPT>(x, sq, sk, ty, tx);
+        dot_rows<D, RPT>(y, sg, sv, ty, tx);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RPT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[i][j] *= sc;
         grad_scores(x, y, s, stats, stats + kPT, r0, c0, ty, tx, a.causal, false);
         put_weights(sp, y, ty, tx);
-        weigh_rows<D>(gq, sp, sk, ty, tx);
+        weigh_rows<D, RPT>(gq, sp, sk, ty, tx);
     }
     copies_wait();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 4 * ty + i;
+    for (int i = 0; i < RPT; ++i) {
+        const int r = r0 + RPT * ty + i;
         if (r < s.nq) write_row<D>(static_cast<float *>(a.dq) + ((s.q0 + r) * a.bt.Hq + h) * D, gq[i], tx, a.scale);
     }
 }
@@ -424,7 +439,7 @@ template <int D, int ROWS> cudaError_t launch_prompt_rows(const PromptArgs &a, c
     constexpr int smem = PromptCfg<D>::smem(ROWS, 1);
     cudaError_t e = allow_smem(attn_prompt_kernel<D, ROWS>, smem);
     if (e != cudaSuccess) return e;
-    attn_prompt_kernel<D, ROWS><<<dim3((unsigned)tiles, a.bt.Hq), ROWS * 4, smem, st>>>(a);
+    attn_prompt_kernel<D, ROWS><<<dim3((unsigned)tiles, a.bt.Hq), RowsCfg<ROWS>::kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -434,22 +449,12 @@ template <int D> cudaError_t launch_prompt(const PromptArgs &a, int sms, cudaStr
                                                                        : launch_prompt_rows<D, 64>(a, st);
 }
 
-template <int D> cudaError_t launch_delta(const PromptArgs &a, cudaStream_t st) {
-    constexpr int LANES = D / 4;
-    const int64_t rows = a.bt.cu_q ? 1 : a.bt.n;
-    const int64_t items_q = rows * a.bt.Tq * a.bt.Hq, items_k = a.bt.cu_k ? rows * a.bt.Tk * a.bt.Hkv : 0;
-    const int64_t items = items_q > items_k ? items_q : items_k;
-    if (items == 0) return cudaSuccess;
-    attn_delta_kernel<D><<<(unsigned)((items * LANES + 255) / 256), 256, 0, st>>>(a);
-    return cudaGetLastError();
-}
-
 template <int D, int ROWS> cudaError_t launch_grad_kv(const PromptArgs &a, cudaStream_t st) {
     constexpr int smem = PromptCfg<D>::smem(ROWS, 2);
     cudaError_t e = allow_smem(attn_grad_kv_kernel<D, ROWS>, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = max_tiles(a.bt.cu_k, a.bt.n, a.bt.Tk, ROWS);
-    attn_grad_kv_kernel<D, ROWS><<<dim3((unsigned)tiles, a.bt.Hkv), ROWS * 4, smem, st>>>(a);
+    attn_grad_kv_kernel<D, ROWS><<<dim3((unsigned)tiles, a.bt.Hkv), RowsCfg<ROWS>::kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 template <int D, int ROWS> cudaError_t launch_grad_q(const PromptArgs &a, cudaStream_t st) {
@@ -457,18 +462,18 @@ template <int D, int ROWS> cudaError_t launch_grad_q(const PromptArgs &a, cudaSt
     cudaError_t e = allow_smem(attn_grad_q_kernel<D, ROWS>, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = max_tiles(a.bt.cu_q, a.bt.n, a.bt.Tq, ROWS);
-    attn_grad_q_kernel<D, ROWS><<<dim3((unsigned)tiles, a.bt.Hq), ROWS * 4, smem, st>>>(a);
+    attn_grad_q_kernel<D, ROWS><<<dim3((unsigned)tiles, a.bt.Hq), RowsCfg<ROWS>::kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 template <int D> cudaError_t launch_prompt_grad(const PromptArgs &a, int sms, cudaStream_t st) {
-    cudaError_t e = launch_delta<D>(a, st);
+    cudaError_t e = cudaSuccess;
+    if (a.bt.Tq > 0)   // first: it forms the delta that the other reads
+        e = prompt_rows(a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq, sms) == 16 ? launch_grad_q<D, 16>(a, st)
+                                                                        : launch_grad_q<D, 64>(a, st);
     if (e == cudaSuccess && a.bt.Tk > 0)
         e = prompt_rows(a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv, sms) == 16 ? launch_grad_kv<D, 16>(a, st)
                                                                          : launch_grad_kv<D, 64>(a, st);
-    if (e == cudaSuccess && a.bt.Tq > 0)
-        e = prompt_rows(a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq, sms) == 16 ? launch_grad_q<D, 16>(a, st)
-                                                                        : launch_grad_q<D, 64>(a, st);
     return e;
 }
 
