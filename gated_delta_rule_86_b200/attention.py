@@ -43,22 +43,25 @@ def kda_attn_fwd(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal=True, scale
     query that sees none gets zeros.  scale: 1 / sqrt(d) by default.  Returns out [B, Tq, Hq, d] in the
     inputs' dtype, with ``return_lse`` also the fp32 [B, Hq, Tq] logarithms of the softmax sums, with
     ``return_rest`` also what rounding took from a bf16 out (None for fp32), for :func:`kda_attn_bwd`.  Rows
-    behind the last packed sequence are not written.
+    behind the last packed sequence are not written.  Sequences never mix, whatever they hold; inside one,
+    keys and values that the causal mask hides must be finite (a hidden row counts with weight zero, which a
+    NaN survives).
     """
     return _native().fwd(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale, out, return_lse, return_rest)
 
 
 def kda_attn_bwd(q, k, v, out, lse, d_out, cu_seqlens=None, cu_seqlens_k=None, causal=True, scale=None, out_rest=None):
     """Gradient of :func:`kda_attn_fwd`: ``(dq, dk, dv)`` in the inputs' dtype, from the forward's inputs,
-    its ``out`` and ``lse`` (and ``out_rest``, which takes a third off the error of bf16 dq and dk), and ``d_out``.  dk and dv are summed over the query heads that share them.
-    Rows behind the last packed sequence get zeros.  The same call gives the same bits."""
+    its ``out`` and ``lse`` (and ``out_rest``: without it bf16 dq errs by up to a fifth more), and ``d_out``.
+    dk and dv are summed over the query heads that share them.  Rows behind the last packed sequence get zeros.  The same call gives the same bits."""
     return _native().bwd(q, k, v, out, lse, d_out, cu_seqlens, cu_seqlens_k, causal, scale, out_rest)
 
 
 def kda_attn(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal=True, scale=None):
     """Differentiable attention over whole prompts: :func:`kda_attn_fwd` with gradients for q, k and v
     (through :func:`kda_attn_bwd`).  Rows of the output behind the last packed sequence are not written
-    and must not reach the loss.  Differentiable once: a backward pass with ``create_graph=True`` raises."""
+    and must not reach the loss.  Differentiable once: a backward pass with ``create_graph=True`` raises.
+    Under CUDA graph capture it raises while an autograd graph of the same leaves lives on another stream."""
     return _native().attn(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale)
 
 

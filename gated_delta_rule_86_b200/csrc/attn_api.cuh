@@ -257,8 +257,9 @@ kda_status kda_attn_bwd_workspace_size(int32_t B, int32_t Tq, int32_t Hq, size_t
 kda_status kda_attn_bwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
                         int64_t v_stride, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int32_t num_seqs,
                         int32_t B, int32_t Tq, int32_t Tk, int32_t Hq, int32_t Hkv, int32_t d, int32_t causal,
-                        float scale, kda_dtype dtype, const void *out, const void *out_rest, const float *lse, const void *d_out, void *dq,
-                        void *dk, void *dv, void *workspace, size_t workspace_bytes, void *stream) {
+                        float scale, kda_dtype dtype, const void *out, const void *out_rest, const float *lse,
+                        const void *d_out, void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes,
+                        void *stream) {
     using namespace kda::attn;
     PromptArgs a = {};
     const kda_status s = check_prompt(a, q, k, v, q_stride, k_stride, v_stride, cu_seqlens_q, cu_seqlens_k, num_seqs,

@@ -11,8 +11,9 @@
 // It is reduced to a fraction of a turn there, and sine and cosine of that are taken in 32 bits (error
 // below 2^-22 against the 2^-9 of the bf16 result).  One sine and cosine serve all heads of a token.
 //
-// Bound by memory: every byte is read once and written once, 16 bytes per thread and access.  A block
-// takes kTokens tokens so that their sines are computed by all of its threads together.
+// Bound by memory: every byte is read once and written once, 16 bytes per thread and access: 8 prompts of
+// 1024 to 16384 tokens, 32 + 8 heads of 128, k_out too: 196 us, 5.9 TB/s.  A step of 256 tokens takes 4.3 us,
+// one of a single token 2.8: the launch and one round trip to memory each for lengths, pages and rows.
 #pragma once
 
 #include "attn_common.cuh"
@@ -184,8 +185,9 @@ __global__ void __launch_bounds__(kAppendThreads) attn_append_kernel(const Appen
 }
 
 template <typename T, int D> cudaError_t launch_append_d(const AppendArgs &a, cudaStream_t st) {
-    // few tokens: one per block, so that they spread over the SMs; many: four, whose sines (up to 64
-    // each) keep all 256 threads busy at once
+    // few tokens: one per block, so that they spread over the SMs; many: four, whose sines (up to 64 each)
+    // keep all 256 threads busy at once.  One against four, 32 + 8 heads of 128: 3.3 and 5.7 us at 16 tokens,
+    // 5.2 and 5.9 at 592, 8.4 and 11.7 at 1184, 15.2 and 12.9 at 2368, 98 and 77 at 16384.
     if (a.tokens <= 148 * 8)
         return launch_behind(attn_append_kernel<T, D, 1>, (unsigned)a.tokens, kAppendThreads, 0, st, a);
     return launch_behind(attn_append_kernel<T, D, 4>, (unsigned)((a.tokens + 3) / 4), kAppendThreads, 0, st, a);

@@ -4,8 +4,10 @@
 // device's current stream to libkda_b200.so.  It is native because a decode step takes 3 to 7 us on the GPU
 // and the same steps in Python took 10 us more on the host than the launch itself; the gradient's half
 // runs on autograd's thread without the interpreter.
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/variable.h>
 #include <torch/extension.h>
 
 #include <cmath>
@@ -213,6 +215,20 @@ std::tuple<Tensor, Tensor, Tensor> bwd(const Tensor &q, const Tensor &k, const T
     return {dq, dk, dv};
 }
 
+// A leaf's gradient is added on the stream on which the first graph that uses the leaf was built, for as long
+// as that graph lives.  While it lives elsewhere, a captured backward pass would have to wait for a stream
+// that is not part of the capture: the process ends in that wait, so the call is refused before.
+void check_capture(const Tensor &t) {
+    if (!t.requires_grad() || !t.is_leaf()) return;
+    const auto sum = torch::autograd::impl::try_get_grad_accumulator(t);
+    if (!sum) return;
+    const c10::cuda::CUDAGuard guard(t.device());
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return;
+    TORCH_CHECK(sum->input_metadata(0).stream() == c10::cuda::getCurrentCUDAStream(t.device().index()).unwrap(),
+                "kda_attn under capture: an autograd graph of the same leaves lives on another stream; free it first, "
+                "or capture kda_attn_fwd and kda_attn_bwd");
+}
+
 // kda_attn_fwd with kda_attn_bwd as its gradient.
 struct Attention : torch::autograd::Function<Attention> {
     static Tensor forward(torch::autograd::AutogradContext *ctx, const Tensor &q, const Tensor &k, const Tensor &v,
@@ -383,7 +399,12 @@ PYBIND11_MODULE(_attention, m) {
     });
     m.def("bwd", &bwd);
     m.def("attn", [](const Tensor &q, const Tensor &k, const Tensor &v, const OptTensor &cu, const OptTensor &cu_k, bool causal,
-                     std::optional<double> scale) { return Attention::apply(q, k, v, cu, cu_k, causal, scale); });
+                     std::optional<double> scale) {
+        const bool graph = at::GradMode::is_enabled() && (q.requires_grad() || k.requires_grad() || v.requires_grad());
+        if (!graph) return std::get<0>(fwd(q, k, v, cu, cu_k, causal, scale, std::nullopt, false, false));
+        for (const Tensor *t : {&q, &k, &v}) check_capture(*t);
+        return Attention::apply(q, k, v, cu, cu_k, causal, scale);
+    });
     m.def("kv_append", &kv_append);
     m.def("decode_step", [](const Tensor &q, const Tensor &kc, const Tensor &vc, const Tensor &table, const Tensor &lens,
                             std::optional<double> scale, const OptTensor &out, bool return_lse) -> py::object {

@@ -208,8 +208,8 @@ __device__ __forceinline__ bool place_of(const int32_t *cu, int nseq, int T, int
     return false;
 }
 
-// Keys [lo, hi) that some query of rows [r0, r1) of a sequence sees: with causal masking query i sees
-// keys j <= i + nk - nq, so that the last query sees the last key.
+// Keys that query `row` of a sequence sees, counted from the first: with causal masking query i sees keys
+// j <= i + nk - nq, so that the last query sees the last key.
 __device__ __forceinline__ int keys_seen(const Seq &s, int row, bool causal) {
     return causal ? min(s.nk, max(0, row + 1 + s.nk - s.nq)) : s.nk;
 }

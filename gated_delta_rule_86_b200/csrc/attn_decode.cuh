@@ -1,14 +1,16 @@
-// attn_decode.cuh -- attention of one new token per sequence over a paged key-value cache.
+// attn_decode.cuh -- attention of one new token per sequence over a paged key-value cache: the schedule, the
+// kernel for fp32 and the one that joins the parts.  (attn_decode_mma.cuh has the kernel for bf16.)
 //
 //     o_h = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q_h . k_j - m),   j = 0 .. seq_lens[b] - 1,
 // one pass over the keys and values with a running maximum m and sum; the query heads of a group share
 // a head of the cache, so a block handles up to GC of them against keys it has loaded once.
 //
 // Bound by memory: the cache is read once.  The work of all (sequence, head) pairs is one line of tiles
-// of 64 tokens, cut into equal shares, one per block: long and short sequences balance, and a single
+// of 64 tokens (bf16: 128), cut into equal shares, one per block: long and short sequences balance, and a single
 // long sequence spreads over the whole GPU.  A share may begin and end inside a pair; such a pair's
 // blocks leave (m, sum, o) in the workspace and a second small kernel joins them in a fixed order (no
-// atomics: the same call gives the same bits).  The lengths stay on the device: every block works out its share from them.
+// atomics: the same call gives the same bits).  The lengths stay on the device: every block works out its
+// share from them.
 //
 // Inside a block each warp runs on its own: it takes 16 of a tile's 64 tokens and copies them through
 // its own ring of stages (cp.async, rows looked up page by page, rows past the end or on a bad page
@@ -177,8 +179,8 @@ template <int TILE> struct Walk {
     __device__ __forceinline__ bool more() const { return at < last; }
 };
 
-template <typename T, int D, int GC> struct DecodeCfg {
-    static constexpr int kRowBytes = D * (int)sizeof(T);
+template <int D, int GC> struct DecodeCfg {
+    static constexpr int kRowBytes = D * 4;
     static constexpr int kStageBytes = 2 * kWarpTokens * kRowBytes;   // keys and values of a warp's tokens
     static constexpr int kStages = 3;
     static constexpr int kDecodeWarps = 4;
@@ -241,23 +243,13 @@ __device__ __forceinline__ uint32_t load_tokens(const DecodeArgs &a, const Walk<
 
 // Channels [4 i, 4 i + 4) of a row staged by load_tokens.
 template <int D> __device__ __forceinline__ float4 staged4(const float *rows, int r, int i) {
-    constexpr int CH = D * 4 / 16;
-    const int c = i;
-    return *reinterpret_cast<const float4 *>(reinterpret_cast<const char *>(rows) + r * (CH * 16) +
-                                             (((c & ~7) | ((c ^ r) & 7)) << 4));
-}
-template <int D> __device__ __forceinline__ float4 staged4(const __nv_bfloat16 *rows, int r, int i) {
-    constexpr int CH = D * 2 / 16;
-    const int c = i >> 1;
-    const uint2 u = *reinterpret_cast<const uint2 *>(reinterpret_cast<const char *>(rows) + r * (CH * 16) +
-                                                     (((c & ~7) | ((c ^ r) & 7)) << 4) + (i & 1) * 8);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
+    return *reinterpret_cast<const float4 *>(reinterpret_cast<const char *>(rows) + r * (D * 4) +
+                                             (((i & ~7) | ((i ^ r) & 7)) << 4));
 }
 
-template <typename T, int D, int GC>
-__global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) attn_decode_kernel(const DecodeArgs a) {
-    using C = DecodeCfg<T, D, GC>;
+template <int D, int GC>
+__global__ void __launch_bounds__(DecodeCfg<D, GC>::kDecodeWarps * 32, 1) attn_decode_kernel(const DecodeArgs a) {
+    using C = DecodeCfg<D, GC>;
     constexpr int kDecodeWarps = C::kDecodeWarps;
     extern __shared__ __align__(1024) uint8_t smem[];
     float *s_q = reinterpret_cast<float *>(smem + C::kRing);
@@ -275,7 +267,7 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
     const bool work = w.start(a, scratch);
     if (a.per_pair && tid == 0) check_len(a, w.b);
     if (!work) {
-        if (a.per_pair) write_empty<T, D, GC>(a, w.b, w.vh);
+        if (a.per_pair) write_empty<float, D, GC>(a, w.b, w.vh);
         return;
     }
     Walk<C::kTile> ahead = w;
@@ -287,7 +279,7 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
 #pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s) {
         if (ahead.more()) {
-            valid[s] = load_tokens<T, D, C::kTile>(a, ahead, warp, lane, ahead.vh / chunks, ring + s * C::kStageBytes);
+            valid[s] = load_tokens<float, D, C::kTile>(a, ahead, warp, lane, ahead.vh / chunks, ring + s * C::kStageBytes);
             ahead.next(a);
         }
         cp_async_commit();
@@ -306,8 +298,7 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
             __syncthreads();
             for (int e = tid; e < GC * D; e += blockDim.x) {
                 const int g = e / D;
-                s_q[e] = g < nh ? to_f32(static_cast<const T *>(a.q)[w.b * a.q_stride + (int64_t)h0 * D + e]) *
-                                      (a.scale * kLog2e)
+                s_q[e] = g < nh ? static_cast<const float *>(a.q)[w.b * a.q_stride + (int64_t)h0 * D + e] * (a.scale * kLog2e)
                                 : 0.f;
             }
             __syncthreads();
@@ -325,7 +316,7 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
             const int into = (st + C::kStages - 1) % C::kStages;
             uint32_t got = 0;
             if (ahead.more()) {
-                got = load_tokens<T, D, C::kTile>(a, ahead, warp, lane, ahead.vh / chunks, ring + into * C::kStageBytes);
+                got = load_tokens<float, D, C::kTile>(a, ahead, warp, lane, ahead.vh / chunks, ring + into * C::kStageBytes);
                 ahead.next(a);
             }
             cp_async_commit();
@@ -339,8 +330,8 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
 #pragma unroll
         for (int s = 0; s < C::kStages; ++s)
             if (s == st) ok = valid[s];
-        const T *ks = reinterpret_cast<const T *>(ring_ptr + st * C::kStageBytes);
-        const T *vs = ks + kWarpTokens * D;
+        const float *ks = reinterpret_cast<const float *>(ring_ptr + st * C::kStageBytes);
+        const float *vs = ks + kWarpTokens * D;
 
         // scores: lane (row, half) sums half of the channels of one key
         float s[GC];
@@ -426,7 +417,7 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, GC>::kDecodeWarps * 32, 1) att
                 }
                 if (whole) {
                     const int64_t h = (int64_t)cur.b * a.Hq + h0 + g;
-                    static_cast<T *>(a.out)[h * D + c] = from_f32<T>(sum > 0.f || sum != sum ? acc / sum : 0.f);
+                    static_cast<float *>(a.out)[h * D + c] = sum > 0.f || sum != sum ? acc / sum : 0.f;
                     if (c == 0 && a.lse)
                         a.lse[h] = sum == 0.f ? -CUDART_INF_F : top * 0.69314718055994531f + logf(sum);
                 } else {

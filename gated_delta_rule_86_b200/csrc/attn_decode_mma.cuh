@@ -9,6 +9,8 @@
 //     O (16 x d) += P V        P from S's own registers, rounded to bf16, the operand type of V
 // tcgen05 would want 64 or 128 rows and its operands through Tensor Memory for the same few products;
 // the kernel is bound by the cache's bytes, not by these.
+// Measured, heads of 128, 4 query heads to one of the cache: 64 sequences of 64 to 16384 tokens 136 us, 6.1 TB/s;
+// one of 131071 tokens 95 us, 5.7 TB/s (some 8 us of it are the start of a share, the last join and its launch).
 #pragma once
 
 #include "attn_decode.cuh"
@@ -326,6 +328,9 @@ inline int decode_group_chunk(int group, bool bf16) {
 
 // Short contexts of few pairs: a block takes a whole pair, which saves the join and its launch.  `tokens`:
 // what a row of the page table can hold.
+// Shares and whole pairs, heads of 128, one sequence and 4 heads of the cache: 8.4 and 5.2 us at 256 tokens,
+// 11.0 and 11.7 at 1024, 12.7 and 20.0 at 2048; 16 sequences and 8 heads: 12.2 and 5.7, 18.9 and 12.5, 32.4 and
+// 24.6 (pairs almost fill the SMs there, but only while their lengths are alike).
 constexpr int kPairTokens = 1024;
 inline int64_t decode_pairs(int64_t n, int Hq, int Hkv, bool bf16) {
     const int group = Hq / Hkv, gc = decode_group_chunk(group, bf16);
@@ -360,10 +365,10 @@ template <int D> cudaError_t launch_attn_decode_bf16(const DecodeArgs &a, int sm
 
 template <int D> cudaError_t launch_attn_decode_f32(const DecodeArgs &a, int sms, cudaStream_t st) {
     switch (decode_group_chunk(a.Hq / a.Hkv, false)) {
-        case 1: return launch_decode_g<float, D, 1, DecodeCfg<float, D, 1>>(attn_decode_kernel<float, D, 1>, 128, a, sms, st);
-        case 2: return launch_decode_g<float, D, 2, DecodeCfg<float, D, 2>>(attn_decode_kernel<float, D, 2>, 128, a, sms, st);
-        case 4: return launch_decode_g<float, D, 4, DecodeCfg<float, D, 4>>(attn_decode_kernel<float, D, 4>, 128, a, sms, st);
-        default: return launch_decode_g<float, D, 8, DecodeCfg<float, D, 8>>(attn_decode_kernel<float, D, 8>, 128, a, sms, st);
+        case 1: return launch_decode_g<float, D, 1, DecodeCfg<D, 1>>(attn_decode_kernel<D, 1>, 128, a, sms, st);
+        case 2: return launch_decode_g<float, D, 2, DecodeCfg<D, 2>>(attn_decode_kernel<D, 2>, 128, a, sms, st);
+        case 4: return launch_decode_g<float, D, 4, DecodeCfg<D, 4>>(attn_decode_kernel<D, 4>, 128, a, sms, st);
+        default: return launch_decode_g<float, D, 8, DecodeCfg<D, 8>>(attn_decode_kernel<D, 8>, 128, a, sms, st);
     }
 }
 

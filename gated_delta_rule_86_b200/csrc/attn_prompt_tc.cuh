@@ -29,6 +29,11 @@
 // The ring of loads runs on from item to item, and an item's first products start under the end of the one
 // before: a block per item cost 7.5 us (d = 64) to 9 us (128) of coming up and running dry, as much as 5 turns.
 //
+// Bound by the tensor pipe and the powers together, which take about the same time at d = 128 and the powers
+// longer at 64.  One prompt of 16384 tokens, 32 heads of 128: 2.1 ms, 1.05 PFLOP/s of visible pairs (three
+// quarters of what a library product sustains under the power limit); 8 packed prompts of 64 to 4096, heads of
+// 64: 243 us; 200 tokens: 11 us, of which a launch, one TMA round trip and two turns in a row.
+//
 // Rows past the end of a sequence in its last tile are another sequence's (or whatever lies behind):
 // their scores are masked, and their values are zeroed in shared memory before the product, since a
 // weight of zero does not hide a NaN.
@@ -194,13 +199,6 @@ template <int D> __device__ __forceinline__ void chain_ss(uint32_t d, uint64_t x
         mma_ss(d, x + step, y + step, idesc, kk > 0, leader);
     }
 }
-// d (+)= x y: x the operand in Tensor Memory over 128 columns, y an MN-major tile.
-__device__ __forceinline__ void chain_ts(uint32_t d, uint32_t x, uint64_t y, uint32_t idesc, bool accumulate, uint32_t leader) {
-#pragma unroll
-    for (int kk = 0; kk < kTile / 16; ++kk)
-        mma_ts(d, x + operand_col(kk), y + kk * 128, idesc, accumulate || kk > 0, leader);
-}
-
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }

@@ -348,8 +348,8 @@ kda_status kda_chunk_bwd_workspace_size(int32_t N, int32_t H, int64_t total_toke
  *   out_rest      : NULL, or bf16 [B, Tq, Hq, d] (bf16 calls only): what rounding
  *                   took from out, for a more exact gradient.
  * A sequence never sees another's keys, whatever they hold (NaN included).
- * Inside a sequence, keys and values that the causal mask hides must be finite
- * for bf16: a hidden value enters the tensor cores' sums with weight zero.
+ * Inside a sequence, keys and values that the causal mask hides must be finite:
+ * a hidden row of a tile enters the sums with weight zero, which a NaN survives.
  */
 kda_status kda_attn_fwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
                         int64_t v_stride, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
@@ -364,10 +364,11 @@ kda_status kda_attn_fwd(const void *q, const void *k, const void *v, int64_t q_s
  *     dV = P^T dO,   dK = scale dS^T Q,   dQ = scale dS K
  * with dK and dV summed over the query heads of a group.  Takes the forward's
  * inputs, its out and lse, out_rest (or NULL: delta is then formed from the
- * rounded out, and dQ and dK err by up to a third more), and d_out [B, Tq, Hq, d] (dense); writes dq [B, Tq,
- * Hq, d], dk and dv [B, Tk, Hkv, d] in the inputs' type.  Rows behind the last
- * packed sequence get zero gradients.  The order of every sum is fixed: the
- * same call gives the same bits.  workspace: kda_attn_bwd_workspace_size bytes.
+ * rounded out, and dQ errs by up to a fifth more), and d_out [B, Tq, Hq, d]
+ * (dense); writes dq [B, Tq, Hq, d], dk and dv [B, Tk, Hkv, d] in the inputs'
+ * type.  Rows behind the last packed sequence get zero gradients.  The order of
+ * every sum is fixed: the same call gives the same bits.
+ * workspace: kda_attn_bwd_workspace_size bytes.
  */
 kda_status kda_attn_bwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
                         int64_t v_stride, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,

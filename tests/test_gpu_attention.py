@@ -341,6 +341,16 @@ def test_decode_many_sequences(n):
     assert torch.equal(out, kda.kda_attn_decode_step(q, kc, vc, table, seq))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_decode_shared_pages(dtype):
+    """Sequences with a prefix in common name its pages twice."""
+    lens = [200, 170, 129, 128, 64]
+    kc, vc, table = cache_of(lens, 2, 64, 64, dtype, 250, fill=float("nan"))
+    for n, shared in ((1, 2), (2, 2), (3, 2), (4, 1)):
+        table[n, :shared] = table[0, :shared]
+    check_decode(make((len(lens), 4, 64), 251, dtype), kc, vc, table, lens)
+
+
 def test_decode_reads_one_pool_and_strided_queries():
     """Keys and values interleaved page by page in one tensor, queries a slice of a projection."""
     lens = [90, 200]
@@ -688,6 +698,38 @@ def test_gradient_in_a_graph_beside_an_eager_one():
     want = torch.autograd.grad(alive, (q, k, v), g)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     torch.cuda.synchronize()
+
+
+def test_captured_gradient_of_live_leaves_is_refused():
+    """Capture of the differentiable call: refused while an eager graph of its leaves lives, sound without one."""
+    q, k, v = (make((1, 70, h, 64), 840 + i, BF16).requires_grad_() for i, h in enumerate((4, 2, 2)))
+    g = make(q.shape, 845, BF16)
+    alive = kda.kda_attn(q, k, v)
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="another stream"), torch.cuda.graph(graph):
+        kda.kda_attn(q, k, v)
+    want = torch.autograd.grad(alive, (q, k, v), g)
+    del alive
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = kda.kda_attn(q, k, v)
+        got = torch.autograd.grad(out, (q, k, v), g)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del out, got
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_differentiable_call_without_a_graph(dtype):
+    q, k, v = (make((2, 50, h, 64), 850 + i, dtype).requires_grad_() for i, h in enumerate((4, 2, 2)))
+    with torch.no_grad():
+        out = kda.kda_attn(q, k, v)
+    assert not out.requires_grad and torch.equal(out, kda.kda_attn(q, k, v))
+    assert torch.equal(out, kda.kda_attn(q.detach(), k.detach(), v.detach()))
 
 
 @pytest.mark.parametrize("d", [64, 128])
