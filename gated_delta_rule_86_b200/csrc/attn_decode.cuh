@@ -261,8 +261,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, GC>::kDecodeWarps * 32, 1) attn_d
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kStages * C::kStageBytes;
     const uint8_t *ring_ptr = smem + warp * C::kStages * C::kStageBytes;
 
-    next_may_start();
+    if (a.per_pair) next_may_start();
     wait_for_previous();
+    if (!a.per_pair) next_may_start();   // only now: the join reads the lengths before its own wait
     Walk<C::kTile> w;
     const bool work = w.start(a, scratch);
     if (a.per_pair && tid == 0) check_len(a, w.b);
@@ -446,7 +447,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
     __shared__ int64_t scratch[20];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x / a.vheads, vh = blockIdx.x % a.vheads;
     next_may_start();
-    wait_for_previous();
+    // The lengths are older than the kernel before this one, which lets this one start when it has itself
+    // waited for them; so the shares are worked out while it runs.
     int64_t all = 0, before = 0;
     for (int n = tid; n < a.n; n += blockDim.x) {
         const int t = decode_units<TILE>(a, n);
@@ -458,14 +460,15 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
     const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv, hkv = vh / chunks, h0 = hkv * group + (vh % chunks) * GC;
     const int nh = min(GC, hkv * group + group - h0);
     const int tiles = decode_tiles<TILE>(a, b);
+    const Shares sh(all, a.blocks);
+    const int64_t s0 = before + (int64_t)vh * (tiles + kPairCost);
+    const int c0 = tiles > 0 ? (int)sh.of(s0) : 0, c1 = tiles > 0 ? (int)sh.of(s0 + tiles - 1) : 0;
+    wait_for_previous();
     if (tid == 0 && vh == 0) check_len(a, b);
     if (tiles == 0) {
         write_empty<T, D, GC>(a, b, vh);
         return;
     }
-    const Shares sh(all, a.blocks);
-    const int64_t s0 = before + (int64_t)vh * (tiles + kPairCost);
-    const int c0 = (int)sh.of(s0), c1 = (int)sh.of(s0 + tiles - 1);
     if (c0 == c1) return;   // one block had it all and wrote the output
     for (int g = warp; g < nh; g += kJoinThreads / 32) {
         // the first block's part lies in its slot 0 if the pair began before its share; the others' in slot 0

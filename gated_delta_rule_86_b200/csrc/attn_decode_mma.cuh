@@ -9,8 +9,8 @@
 //     O (16 x d) += P V        P from S's own registers, rounded to bf16, the operand type of V
 // tcgen05 would want 64 or 128 rows and its operands through Tensor Memory for the same few products;
 // the kernel is bound by the cache's bytes, not by these.
-// Measured, heads of 128, 4 query heads to one of the cache: 64 sequences of 64 to 16384 tokens 136 us, 6.1 TB/s;
-// one of 131071 tokens 95 us, 5.7 TB/s (some 8 us of it are the start of a share, the last join and its launch).
+// Measured, heads of 128, 4 query heads to one of the cache: 64 sequences of 64 to 16384 tokens 135 us, 6.2 TB/s;
+// one of 131071 tokens 94 us, 5.7 TB/s (some 8 us of it are the start of a share, the last join and its launch).
 #pragma once
 
 #include "attn_decode.cuh"
@@ -91,8 +91,9 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
     const int gr = lane >> 2, gc = lane & 3;   // a fragment's row and column pair
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kStages * C::kStageBytes;
 
-    next_may_start();
+    if (a.per_pair) next_may_start();
     wait_for_previous();
+    if (!a.per_pair) next_may_start();   // only now: the join reads the lengths before its own wait
     Walk<C::kTile> w;
     const bool work = w.start(a, scratch);
     if (a.per_pair && tid == 0) check_len(a, w.b);
