@@ -329,9 +329,9 @@ inline int decode_group_chunk(int group, bool bf16) {
 
 // Short contexts of few pairs: a block takes a whole pair, which saves the join and its launch.  `tokens`:
 // what a row of the page table can hold.
-// Shares and whole pairs, heads of 128, one sequence and 4 heads of the cache: 8.4 and 5.2 us at 256 tokens,
-// 11.0 and 11.7 at 1024, 12.7 and 20.0 at 2048; 16 sequences and 8 heads: 12.2 and 5.7, 18.9 and 12.5, 32.4 and
-// 24.6 (pairs almost fill the SMs there, but only while their lengths are alike).
+// Shares and whole pairs, heads of 128, one sequence and 4 heads of the cache: 7.3 and 4.9 us at 256 tokens,
+// 9.7 and 10.5 at 1024, 11.4 and 17.9 at 2048; 16 sequences and 8 heads: 10.3 and 5.6, 15.8 and 11.4, 29.3 and
+// 24.0 (pairs almost fill the SMs there, but only while their lengths are alike).
 constexpr int kPairTokens = 1024;
 inline int64_t decode_pairs(int64_t n, int Hq, int Hkv, bool bf16) {
     const int group = Hq / Hkv, gc = decode_group_chunk(group, bf16);
