@@ -17,7 +17,7 @@
 // RPT ty and on, so a row's 16 threads lie in one half of a warp and its maximum and sum are four shuffles.
 // Large batches have 64 rows a block and 4 a thread (16 products for 8 loads from shared memory), small
 // ones 16 and 2 (4 warps; with 1 a thread and 8 warps shared memory is read more and the time is the same:
-// B1 T256 H2 D64 14 us forward, 43 gradient, against 14 and 45).  The next tile is on its way (cp.async) while one is worked on.
+// B1 T256 H2 D64 14 us forward, 43 gradient in two launches, against 14 and 45).  The next tile is on its way (cp.async) while one is worked on.
 #pragma once
 
 #include "attn_append.cuh"
@@ -52,9 +52,9 @@ constexpr int kPT = 64;   // rows of a tile of the other side
 template <int D> struct PromptCfg {
     static constexpr int kPitch = D + 4;           // floats of a staged row
     static constexpr int kTileF = kPT * kPitch;
-    // own tiles of `rows` rows, two tiles of the other side twice, weights [rows][68], statistics
-    static constexpr int smem(int rows, int own) {
-        return (own * rows * kPitch + 4 * kTileF + rows * 68 + 2 * 2 * kPT) * 4 + 160;
+    // own tiles of `rows` rows, `ring` tiles of the other side (two or three, twice), weights [rows][68], statistics
+    static constexpr int smem(int rows, int own, int ring = 4) {
+        return (own * rows * kPitch + ring * kTileF + rows * 68 + 2 * 2 * kPT) * 4 + 160;
     }
 };
 
@@ -247,8 +247,8 @@ __device__ __forceinline__ void grad_scores(float (&x)[RPT][4], float (&y)[RPT][
         }
 }
 
-// lse (in log2 units; 0 for rows that see nothing) and delta of N queries
-template <int N, int THREADS>
+// lse (in log2 units; 0 for rows that see nothing) and delta (where DELTA) of N queries
+template <int N, int THREADS, bool DELTA>
 __device__ __forceinline__ void stage_stats(float *lse2, float *delta, const PromptArgs &a, const Seq &s, int r0, int h) {
     for (int i = threadIdx.x; i < N; i += THREADS) {
         const int r = r0 + i;
@@ -256,11 +256,11 @@ __device__ __forceinline__ void stage_stats(float *lse2, float *delta, const Pro
         if (r < s.nq) {
             const int64_t at = stat_at(a.bt, s.q0 + r, h);
             x = a.lse[at] * kLog2e;
-            y = a.delta[at];
+            if (DELTA) y = a.delta[at];
             if (x == -CUDART_INF_F) x = 0.f;
         }
         lse2[i] = x;
-        delta[i] = y;
+        if (DELTA) delta[i] = y;
     }
 }
 
@@ -275,20 +275,19 @@ template <typename T> __device__ __forceinline__ void zero_behind(T *g, const in
         reinterpret_cast<uint4 *>(g + (int64_t)from * row)[i] = make_uint4(0, 0, 0, 0);
 }
 
-// dK and dV of ROWS keys of one head of the cache, over all query heads of its group.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_grad_kv_kernel(const PromptArgs a) {
+// dK and dV of ROWS keys (the index-th tile) of one head of the cache, over all query heads of its group.
+// OWN_DELTA: delta is formed here from O, for a launch beside the queries' blocks.
+template <int D, int ROWS, bool OWN_DELTA>
+__device__ __forceinline__ void grad_kv(const PromptArgs &a, int64_t index, int hk) {
     using C = PromptCfg<D>;
-    constexpr int THREADS = RowsCfg<ROWS>::kThreads, RPT = RowsCfg<ROWS>::kPer;
+    constexpr int THREADS = RowsCfg<ROWS>::kThreads, RPT = RowsCfg<ROWS>::kPer, TILES = OWN_DELTA ? 3 : 2;
     extern __shared__ __align__(16) float sm[];
-    float *sk = sm, *sv = sk + ROWS * C::kPitch, *ring = sv + ROWS * C::kPitch, *sp = ring + 4 * C::kTileF,
+    float *sk = sm, *sv = sk + ROWS * C::kPitch, *ring = sv + ROWS * C::kPitch, *sp = ring + 2 * TILES * C::kTileF,
           *stats = sp + ROWS * 68;   // lse and delta of two tiles
     int *scratch = reinterpret_cast<int *>(stats + 4 * kPT);
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, hk = blockIdx.y;
-    zero_behind(static_cast<float *>(a.dk), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
-    zero_behind(static_cast<float *>(a.dv), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     int n, t;
-    if (!find_tile(a.bt.cu_k, a.bt.n, a.bt.Tk, ROWS, blockIdx.x, scratch, n, t)) return;
+    if (!find_tile(a.bt.cu_k, a.bt.n, a.bt.Tk, ROWS, index, scratch, n, t)) return;
     const Seq s = seq_of(a.bt, n);
     const int c0 = t * ROWS, group = a.bt.Hq / a.bt.Hkv;
     // the first tile of queries that sees key c0
@@ -297,13 +296,17 @@ __global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_grad_kv_kernel(c
     auto load = [&](int it, int into) {
         if (it < total) {
             const int h = hk * group + it / per_head, r0 = (start + it % per_head) * kPT;
-            stage_rows<D, kPT, THREADS>(ring + 2 * into * C::kTileF,
+            stage_rows<D, kPT, THREADS>(ring + TILES * into * C::kTileF,
                                         static_cast<const float *>(a.q) + s.q0 * a.q_stride + (int64_t)h * D, a.q_stride,
                                         r0, s.nq);
-            stage_rows<D, kPT, THREADS>(ring + (2 * into + 1) * C::kTileF,
+            stage_rows<D, kPT, THREADS>(ring + (TILES * into + 1) * C::kTileF,
                                         static_cast<const float *>(a.d_out) + (s.q0 * a.bt.Hq + h) * (int64_t)D,
                                         (int64_t)a.bt.Hq * D, r0, s.nq);
-            stage_stats<kPT, THREADS>(stats + 2 * into * kPT, stats + (2 * into + 1) * kPT, a, s, r0, h);
+            if (OWN_DELTA)
+                stage_rows<D, kPT, THREADS>(ring + (TILES * into + 2) * C::kTileF,
+                                            static_cast<const float *>(a.out) + (s.q0 * a.bt.Hq + h) * (int64_t)D,
+                                            (int64_t)a.bt.Hq * D, r0, s.nq);
+            stage_stats<kPT, THREADS, !OWN_DELTA>(stats + 2 * into * kPT, stats + (2 * into + 1) * kPT, a, s, r0, h);
         }
         copies_commit();
     };
@@ -316,10 +319,24 @@ __global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_grad_kv_kernel(c
     float gk[RPT][D / 16] = {}, gv[RPT][D / 16] = {};
     for (int it = 0; it < total; ++it) {
         const int at = it & 1, r0 = (start + it % per_head) * kPT;
-        const float *sq = ring + 2 * at * C::kTileF, *sg = sq + C::kTileF;
+        const float *sq = ring + TILES * at * C::kTileF, *sg = sq + C::kTileF;
         copies_wait();
         __syncthreads();
         load(it + 1, at ^ 1);
+        if (OWN_DELTA) {
+            constexpr int PER = THREADS / kPT;   // threads of a row
+            const int r = tid / PER;
+            const float *go = sg + r * C::kPitch, *oo = sg + C::kTileF + r * C::kPitch;
+            float dot = 0.f;
+#pragma unroll
+            for (int c = (tid % PER) * 4; c < D; c += 4 * PER) {
+                const float4 x = *reinterpret_cast<const float4 *>(go + c), y = *reinterpret_cast<const float4 *>(oo + c);
+                dot += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+            }
+#pragma unroll
+            for (int d = PER / 2; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+            if (tid % PER == 0) stats[(2 * at + 1) * kPT + r] = dot;
+        }
         float x[RPT][4] = {}, y[RPT][4] = {};
         dot_rows<D, RPT>(x, sk, sq, ty, tx);
         dot_rows<D, RPT>(y, sv, sg, ty, tx);
@@ -327,6 +344,7 @@ __global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_grad_kv_kernel(c
         for (int i = 0; i < RPT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[i][j] *= sc;
+        if (OWN_DELTA) __syncthreads();
         grad_scores(x, y, s, stats + 2 * at * kPT, stats + (2 * at + 1) * kPT, r0, c0, ty, tx, a.causal, true);
         put_weights(sp, x, ty, tx);
         weigh_rows<D, RPT>(gv, sp, sg, ty, tx);
@@ -344,19 +362,25 @@ __global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_grad_kv_kernel(c
     }
 }
 
-// dQ of ROWS queries of one head; and their delta = dO . O, which the keys' kernel reads after this one.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_grad_q_kernel(const PromptArgs a) {
+__global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_grad_kv_kernel(const PromptArgs a) {
+    zero_behind(static_cast<float *>(a.dk), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
+    zero_behind(static_cast<float *>(a.dv), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
+    grad_kv<D, ROWS, false>(a, blockIdx.x, blockIdx.y);
+}
+
+// dQ of ROWS queries (the index-th tile) of one head; and their delta = dO . O, which the keys' kernel reads
+// after this one.
+template <int D, int ROWS> __device__ __forceinline__ void grad_q(const PromptArgs &a, int64_t index, int h) {
     using C = PromptCfg<D>;
     constexpr int THREADS = RowsCfg<ROWS>::kThreads, RPT = RowsCfg<ROWS>::kPer;
     extern __shared__ __align__(16) float sm[];
     float *sq = sm, *sg = sq + ROWS * C::kPitch, *ring = sg + ROWS * C::kPitch, *sp = ring + 4 * C::kTileF,
           *stats = sp + ROWS * 68;
     int *scratch = reinterpret_cast<int *>(stats + 4 * kPT);
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, h = blockIdx.y;
-    zero_behind(static_cast<float *>(a.dq), a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq * D);
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     int n, t;
-    if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, ROWS, gridDim.x - 1 - blockIdx.x, scratch, n, t)) return;
+    if (!find_tile(a.bt.cu_q, a.bt.n, a.bt.Tq, ROWS, index, scratch, n, t)) return;
     const Seq s = seq_of(a.bt, n);
     const int r0 = t * ROWS, hk = h / (a.bt.Hq / a.bt.Hkv);
     const float *k = static_cast<const float *>(a.k) + s.k0 * a.k_stride + (int64_t)hk * D;
@@ -428,6 +452,25 @@ __global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_grad_q_kernel(co
     }
 }
 
+template <int D, int ROWS>
+__global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_grad_q_kernel(const PromptArgs a) {
+    zero_behind(static_cast<float *>(a.dq), a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq * D);
+    grad_q<D, ROWS>(a, gridDim.x - 1 - blockIdx.x, blockIdx.y);   // the last tiles see the most keys
+}
+
+// Both for small batches, side by side: neither fills the GPU.  The first blocks take the keys.  B1 T256 H2 D64:
+// 29 us, 45 one after the other; T48 H4 D128 11 and 21; T1024 H2 D64 108 and 158; T1024 H8 D64, where either comes
+// near to filling it alone, 309 and 287.
+template <int D>
+__global__ void __launch_bounds__(RowsCfg<16>::kThreads) attn_grad_both_kernel(const PromptArgs a, int kv_blocks) {
+    zero_behind(static_cast<float *>(a.dk), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
+    zero_behind(static_cast<float *>(a.dv), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
+    zero_behind(static_cast<float *>(a.dq), a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq * D);
+    const int block = blockIdx.x;
+    if (block < kv_blocks) grad_kv<D, 16, true>(a, block / a.bt.Hkv, block % a.bt.Hkv);
+    else grad_q<D, 16>(a, (gridDim.x - 1 - block) / a.bt.Hq, (gridDim.x - 1 - block) % a.bt.Hq);
+}
+
 template <typename K> cudaError_t allow_smem(K kern, int bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
@@ -435,7 +478,8 @@ template <typename K> cudaError_t allow_smem(K kern, int bytes) {
 // Rows of a block: 64, or 16 where blocks of 64 rows would not reach every SM (a tile's work is then
 // spread over four times the blocks, and each is done sooner).  16 against 64, heads of 64, forward and
 // gradient: T256 H2 14 and 43 against 23 and 72 us; T1024 H2 48 and 153 against 80 and 267; T1024 H8 (128 blocks)
-// 87 and 281 against 80 and 268; B4 T1024 H4 (256 blocks) 146 and 480 against 125 and 419.
+// 87 and 281 against 80 and 268; B4 T1024 H4 (256 blocks) 146 and 480 against 125 and 419.  (Gradients in two
+// launches, which attn_grad_both_kernel has improved on for 16 rows.)
 inline int prompt_rows(const int32_t *cu, int n, int T, int heads, int sms) {
     return max_tiles(cu, n, T, 64) * heads < sms ? 16 : 64;
 }
@@ -473,13 +517,22 @@ template <int D, int ROWS> cudaError_t launch_grad_q(const PromptArgs &a, cudaSt
 }
 
 template <int D> cudaError_t launch_prompt_grad(const PromptArgs &a, int sms, cudaStream_t st) {
+    const int rows_q = prompt_rows(a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq, sms),
+              rows_k = prompt_rows(a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv, sms);
+    if (a.bt.Tq > 0 && a.bt.Tk > 0 && rows_q == 16 && rows_k == 16) {
+        constexpr int smem = PromptCfg<D>::smem(16, 2, 6);
+        static_assert(smem <= 232448, "shared memory");
+        const cudaError_t e = allow_smem(attn_grad_both_kernel<D>, smem);
+        if (e != cudaSuccess) return e;
+        const int64_t kv = max_tiles(a.bt.cu_k, a.bt.n, a.bt.Tk, 16) * a.bt.Hkv,
+                      q = max_tiles(a.bt.cu_q, a.bt.n, a.bt.Tq, 16) * a.bt.Hq;
+        attn_grad_both_kernel<D><<<(unsigned)(kv + q), RowsCfg<16>::kThreads, smem, st>>>(a, (int)kv);
+        return cudaGetLastError();
+    }
     cudaError_t e = cudaSuccess;
     if (a.bt.Tq > 0)   // first: it forms the delta that the other reads
-        e = prompt_rows(a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq, sms) == 16 ? launch_grad_q<D, 16>(a, st)
-                                                                        : launch_grad_q<D, 64>(a, st);
-    if (e == cudaSuccess && a.bt.Tk > 0)
-        e = prompt_rows(a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv, sms) == 16 ? launch_grad_kv<D, 16>(a, st)
-                                                                         : launch_grad_kv<D, 64>(a, st);
+        e = rows_q == 16 ? launch_grad_q<D, 16>(a, st) : launch_grad_q<D, 64>(a, st);
+    if (e == cudaSuccess && a.bt.Tk > 0) e = rows_k == 16 ? launch_grad_kv<D, 16>(a, st) : launch_grad_kv<D, 64>(a, st);
     return e;
 }
 

@@ -128,6 +128,19 @@ def test_prompt_gradient_groups(hq, hkv, dtype):
         inside(x, y, t, n)
 
 
+@pytest.mark.parametrize("tq,tk,hq,hkv", [(640, 640, 16, 2), (70, 9500, 1, 1), (300, 40, 3, 1), (40, 300, 2, 2)])
+def test_prompt_gradient_fp32_blocks(tq, tk, hq, hkv):
+    """Queries and keys that differ in the rows of a block, and both small in one launch."""
+    q, k, v, g = (make((1, t, h, 64), 130 + i, FP32) for i, (t, h) in enumerate(((tq, hq), (tk, hkv), (tk, hkv), (tq, hq))))
+    for causal in (True, False):
+        out, lse = kda.kda_attn_fwd(q, k, v, causal=causal, return_lse=True)
+        got = kda.kda_attn_bwd(q, k, v, out, lse, g, causal=causal)
+        want, tols = ref.attention_grad(q, k, v, g, causal=causal)
+        for x, y, t, n in zip(got, want, tols, ("dq", "dk", "dv")):
+            inside(x, y, t, n)
+        assert all(torch.equal(a, b) for a, b in zip(got, kda.kda_attn_bwd(q, k, v, out, lse, g, causal=causal)))
+
+
 def test_prompt_gradient_against_differences():
     """The derivative of a weighted sum of the library's own fp32 outputs along a random direction, by
     central differences: the truncation is of order h^2, the outputs' rounding e / h."""
