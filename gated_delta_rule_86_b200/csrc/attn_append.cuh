@@ -12,7 +12,7 @@
 // below 2^-22 against the 2^-9 of the bf16 result).  One sine and cosine serve all heads of a token.
 //
 // Bound by memory: every byte is read once and written once, 16 bytes per thread and access: 8 prompts of
-// 1024 to 16384 tokens, 32 + 8 heads of 128, k_out too: 196 us, 5.9 TB/s.  A step of 256 tokens takes 4.3 us,
+// 1024 to 16384 tokens, 32 + 8 heads of 128, k_out too: 192 us, 6.0 TB/s.  A step of 256 tokens takes 4.3 us,
 // one of a single token 2.8: the launch and one round trip to memory each for lengths, pages and rows.
 #pragma once
 
@@ -63,8 +63,10 @@ template <typename T> __device__ __forceinline__ void store16(T *p, const Vec16<
     *reinterpret_cast<uint4 *>(p) = c.u;
 }
 
+// Six blocks per SM, 40 registers a thread: 192 us for the prompts above, with five (48 registers) 197, with
+// seven, which spill, 248; two units of a thread under way at once (74 registers, three blocks) 249.
 template <typename T, int D, int TOKENS>
-__global__ void __launch_bounds__(kAppendThreads) attn_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 6) attn_append_kernel(const AppendArgs a) {
     constexpr int VE = Vec16<T>::N;      // elements of a 16-byte vector
     constexpr int UNITS = D / (2 * VE);  // a thread's share of a head: two vectors
     __shared__ float2 s_turn[TOKENS][D / 2];
