@@ -79,10 +79,11 @@ def build_binding(force: bool = False) -> str:
 
 
 def build_probe(force: bool = False) -> str:
-    """Test-only tcgen05 probe library (tests/csrc)."""
-    src = os.path.join(ROOT, "tests", "csrc", "tc_probe.cu")
-    out = os.path.join(ROOT, "tests", "csrc", "libtc_probe.so")
-    return compile_so(src, out, _sources(), force=force)
+    """Test-only probe libraries (tests/csrc): tcgen05 layouts, and parts of the attention kernels."""
+    for name in ("attn_probe", "tc_probe"):
+        out = compile_so(os.path.join(ROOT, "tests", "csrc", f"{name}.cu"), os.path.join(ROOT, "tests", "csrc", f"lib{name}.so"),
+                         _sources(), force=force)
+    return out
 
 
 if __name__ == "__main__":

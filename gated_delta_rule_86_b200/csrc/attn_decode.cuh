@@ -48,9 +48,9 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
 }
 
 // Tokens of sequence b that there are: its length, at most what its row of the table can hold.
-__device__ __forceinline__ int decode_len(const DecodeArgs &a, int b) {
+__host__ __device__ __forceinline__ int decode_len(const DecodeArgs &a, int b) {
     const int64_t most = (int64_t)a.cache.width << a.cache.page_log2;
-    return (int)min((int64_t)max(__ldg(a.lens + b), 0), most);
+    return (int)min((int64_t)max(a.lens[b], 0), most);
 }
 // What a pair costs beside its tiles (its queries, the join of the warps), in tiles: it counts in the shares,
 // or blocks with many short pairs would end long after the others.
@@ -163,7 +163,7 @@ template <int TILE> struct Walk {
         }
         return at < last;
     }
-    __device__ __forceinline__ void next(const DecodeArgs &a) {
+    __host__ __device__ __forceinline__ void next(const DecodeArgs &a) {
         ++at;
         if (++tile < tiles) return;
         at += kPairCost;
@@ -176,7 +176,7 @@ template <int TILE> struct Walk {
         } while (len == 0);
         tiles = (len + TILE - 1) / TILE;
     }
-    __device__ __forceinline__ bool more() const { return at < last; }
+    __host__ __device__ __forceinline__ bool more() const { return at < last; }
 };
 
 template <int D, int GC> struct DecodeCfg {

@@ -38,9 +38,16 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // The page of a warp's first token of a tile, -1 where it has none; its lookup runs a tile ahead of its use.
-template <int TILE> __device__ __forceinline__ int first_page(const DecodeArgs &a, const Walk<TILE> &w, int warp) {
+template <int TILE>
+__host__ __device__ __forceinline__ int first_page(const DecodeArgs &a, const Walk<TILE> &w, int warp) {
     const int tok = w.tile * TILE + warp * kWarpTokens;
-    return tok < w.len ? __ldg(a.cache.table + w.b * a.cache.row + (tok >> a.cache.page_log2)) : -1;
+    return tok < w.len ? a.cache.table[w.b * a.cache.row + (tok >> a.cache.page_log2)] : -1;
+}
+// Moves to the next tile and looks up its page.  Behind the share's end the walk may stand behind the last
+// sequence, where the table has no row.
+template <int TILE> __host__ __device__ __forceinline__ int next_page(const DecodeArgs &a, Walk<TILE> &w, int warp) {
+    w.next(a);
+    return w.more() ? first_page(a, w, warp) : -1;
 }
 
 // load_tokens where the 16 tokens all exist and lie on one good page (`page`): 16 rows side by side in
@@ -111,8 +118,7 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
             load_whole<D, C::kTile>(a, ahead, warp, lane, hkv, stage, page);
         else
             got = tok < ahead.len ? load_tokens<__nv_bfloat16, D, C::kTile>(a, ahead, warp, lane, hkv, stage) : 0;
-        ahead.next(a);
-        page = first_page(a, ahead, warp);
+        page = next_page(a, ahead, warp);
         return got;
     };
     const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv;
