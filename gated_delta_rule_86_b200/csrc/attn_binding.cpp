@@ -270,7 +270,10 @@ int64_t page_step(const Tensor &c) {
     if (c.stride(3) != 1 || (c.size(2) > 1 && c.stride(2) != c.size(3)) ||
         (c.size(1) > 1 && c.stride(1) != c.size(2) * c.size(3)))
         bad_value("a page of the cache must be dense; pages may lie apart");
-    return c.size(0) > 1 ? c.stride(0) : dense;
+    if (c.size(0) < 2) return dense;
+    if (c.stride(0) < dense)   // 0 among them, which the library would take for dense
+        bad_value("the pages of a cache must not overlap: they lie ", c.stride(0), " elements apart and hold ", dense);
+    return c.stride(0);
 }
 
 Paged cache_args(const Tensor &k_cache, const Tensor &v_cache, const Tensor &table, int64_t n) {

@@ -174,3 +174,16 @@ def test_status_becomes_kda_error(lib):
     """The native module raises the package's own error type."""
     err = kda.KdaError(2, "kda_attn_fwd")
     assert err.status == 2 and "KDA_ERR_UNSUPPORTED" in str(err) and isinstance(err, RuntimeError)
+
+
+def test_binding_refuses_caches_whose_pages_overlap(lib):
+    """One page shown several times (a distance of 0, which means dense to the library), and pages that overlap in part."""
+    x = torch.zeros(1, 1, 2, 64)
+    i = torch.zeros(1, dtype=torch.int32)
+    t = torch.zeros(1, 4, dtype=torch.int32)
+    c = torch.zeros(4, 2, 16, 64)
+    for bad in (c[:1].expand(4, -1, -1, -1), torch.zeros(8 * 2 * 16 * 64).as_strided((4, 2, 16, 64), (1024, 1024, 64, 1))):
+        for caches in ((bad, c), (c, bad)):
+            for call in (lambda: kda.kda_kv_append(x, x, *caches, t, i), lambda: kda.kda_attn_decode_step(x[:, 0], *caches, t, i)):
+                with pytest.raises(ValueError, match="overlap"):
+                    call()
