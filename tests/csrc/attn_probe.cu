@@ -2,6 +2,7 @@
 #include <stdint.h>
 
 #include "../../gated_delta_rule_86_b200/csrc/attn_decode_mma.cuh"
+#include "../../gated_delta_rule_86_b200/csrc/attn_prompt_tc.cuh"
 
 using namespace kda::attn;
 
@@ -24,6 +25,17 @@ template <int TILE> int64_t walk(const DecodeArgs &a, int b, int vh, int64_t cou
     }
 }
 
+// The softmax warp and place (16 * place + warp) that gives up; none: -1.
+__device__ int g_quit = -1;
+struct QuitOne {
+    static __device__ __forceinline__ bool gives_up(int warp, int place, volatile int *abort) {
+        if (16 * place + warp != g_quit) return false;
+        kda::record_device_error(kda::kDevErrTimeout);
+        *abort = 1;
+        return true;
+    }
+};
+
 }  // namespace
 
 // On the host, over host memory.
@@ -38,4 +50,34 @@ extern "C" int64_t attn_probe_walk(const int32_t *lens, int n, int vheads, const
     a.cache.width = width;
     a.cache.page_log2 = page_log2;
     return walk<DecodeMmaCfg<128, 8>::kTile>(a, b, vh, count, warp, marker);
+}
+
+// The prompt kernel with one softmax warp of every block giving up (see NoFault).  Synchronises; returns the
+// device error word, which it clears, or -1 if a CUDA call failed.
+extern "C" int attn_probe_give_up(int quit, int d, const void *q, const void *k, const void *v, int B, int T, int Hq, int Hkv,
+                                  float scale, void *out) {
+    PromptArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = (int64_t)Hq * d;
+    a.k_stride = a.v_stride = (int64_t)Hkv * d;
+    a.bt.n = B;
+    a.bt.Tq = a.bt.Tk = T;
+    a.bt.Hq = Hq;
+    a.bt.Hkv = Hkv;
+    a.causal = true;
+    a.scale = scale;
+    a.out = out;
+    int sms = 0, word = 0;
+    const int none = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, 0) != cudaSuccess) return -1;
+    if (cudaMemcpyToSymbol(g_quit, &quit, sizeof(quit)) != cudaSuccess) return -1;
+    if ((d == 64 ? launch_prompt_tc<64, QuitOne>(a, sms, nullptr) : launch_prompt_tc<128, QuitOne>(a, sms, nullptr)) !=
+        cudaSuccess)
+        return -1;
+    if (cudaDeviceSynchronize() != cudaSuccess) return -1;
+    if (cudaMemcpyFromSymbol(&word, kda::g_device_error, sizeof(word)) != cudaSuccess) return -1;
+    if (cudaMemcpyToSymbol(kda::g_device_error, &none, sizeof(none)) != cudaSuccess) return -1;
+    return word;
 }
