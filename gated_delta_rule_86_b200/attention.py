@@ -60,7 +60,8 @@ def kda_attn_bwd(q, k, v, out, lse, d_out, cu_seqlens=None, cu_seqlens_k=None, c
 def kda_attn(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal=True, scale=None):
     """Differentiable attention over whole prompts: :func:`kda_attn_fwd` with gradients for q, k and v
     (through :func:`kda_attn_bwd`).  Rows of the output behind the last packed sequence are not written
-    and must not reach the loss.  Differentiable once: a backward pass with ``create_graph=True`` raises.
+    and must not reach the loss.  Differentiable once: a backward pass with ``create_graph=True`` raises, and
+    so do inputs with tangents of forward-mode differentiation.
     Under CUDA graph capture it raises while an autograd graph of the same leaves lives on another stream."""
     return _native().attn(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale)
 

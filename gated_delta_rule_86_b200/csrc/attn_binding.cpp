@@ -229,6 +229,11 @@ void check_capture(const Tensor &t) {
                 "or capture kda_attn_fwd and kda_attn_bwd");
 }
 
+// A tangent of forward-mode differentiation would be dropped where no input asks for a gradient.
+void check_no_tangent(const Tensor &t) {
+    TORCH_CHECK_NOT_IMPLEMENTED(!t._fw_grad(0).defined(), "kda_attn has no forward-mode derivative: an input carries a tangent");
+}
+
 // kda_attn_fwd with kda_attn_bwd as its gradient.
 struct Attention : torch::autograd::Function<Attention> {
     static Tensor forward(torch::autograd::AutogradContext *ctx, const Tensor &q, const Tensor &k, const Tensor &v,
@@ -403,6 +408,7 @@ PYBIND11_MODULE(_attention, m) {
     m.def("bwd", &bwd);
     m.def("attn", [](const Tensor &q, const Tensor &k, const Tensor &v, const OptTensor &cu, const OptTensor &cu_k, bool causal,
                      std::optional<double> scale) {
+        for (const Tensor *t : {&q, &k, &v}) check_no_tangent(*t);
         const bool graph = at::GradMode::is_enabled() && (q.requires_grad() || k.requires_grad() || v.requires_grad());
         if (!graph) return std::get<0>(fwd(q, k, v, cu, cu_k, causal, scale, std::nullopt, false, false));
         for (const Tensor *t : {&q, &k, &v}) check_capture(*t);

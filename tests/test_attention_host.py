@@ -187,3 +187,18 @@ def test_binding_refuses_caches_whose_pages_overlap(lib):
             for call in (lambda: kda.kda_kv_append(x, x, *caches, t, i), lambda: kda.kda_attn_decode_step(x[:, 0], *caches, t, i)):
                 with pytest.raises(ValueError, match="overlap"):
                     call()
+
+
+def test_forward_mode_is_refused(lib):
+    """An input with a tangent: no derivative of zero without a word (found before the device is looked at)."""
+    import torch.autograd.forward_ad as fwd_ad
+    plain = torch.zeros(1, 4, 2, 64)
+    with fwd_ad.dual_level():
+        dual = fwd_ad.make_dual(plain, torch.ones_like(plain))
+        for i in range(3):
+            args = [plain] * 3
+            args[i] = dual
+            for wants in (False, True):
+                args[(i + 1) % 3] = plain.clone().requires_grad_(wants)
+                with pytest.raises(NotImplementedError, match="forward-mode"):
+                    kda.kda_attn(*args)
