@@ -419,7 +419,7 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
             }
             ++own;
         }
-        if (!ok) {   // no product in flight when the memory is given back
+        if (!ok || *abort) {   // no product in flight when the memory is given back
             int quit = 0;
             commit_by(&bars.drain, leader);
             warp_wait(&bars.drain, 0, &quit);
@@ -653,7 +653,7 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
             }
             ++own;
         }
-        if (!ok) {   // no product in flight when the memory is given back
+        if (!ok || *abort) {   // no product in flight when the memory is given back
             int quit = 0;
             commit_by(&bars.drain, leader);
             warp_wait(&bars.drain, 0, &quit);

@@ -508,7 +508,7 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                 }
                 advance(r);
             }
-            if (!ok) {   // no product in flight when the memory is given back
+            if (!ok || *abort) {   // no product in flight when the memory is given back
                 int quit = 0;
                 commit_by(&bars.drain, leader);
                 warp_wait(&bars.drain, 0, &quit);
