@@ -38,10 +38,10 @@ constexpr int kAppendThreads = 256;
 // sequence of a packed token: the last n with cu[n] <= token; -1 behind the last sequence
 __device__ __forceinline__ int seq_of_token(const int32_t *cu, int n, int64_t token) {
     int lo = 0, hi = n;   // cu[lo] <= token < cu[hi], if there is such a pair
-    if (token < __ldg(cu) || token >= __ldg(cu + n)) return -1;
+    if (token < cu[0] || token >= cu[n]) return -1;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(cu + mid) <= token) lo = mid;
+        if (cu[mid] <= token) lo = mid;
         else hi = mid;
     }
     return lo;
@@ -83,13 +83,13 @@ __global__ void __launch_bounds__(kAppendThreads, 6) attn_append_kernel(const Ap
             int64_t j;
             if (a.cu) {
                 seq = seq_of_token(a.cu, a.n, t);
-                j = seq < 0 ? 0 : t - __ldg(a.cu + seq);
+                j = seq < 0 ? 0 : t - a.cu[seq];
             } else {
                 seq = (int)(t / a.T);
                 j = t - (int64_t)seq * a.T;
             }
             if (seq >= 0) {
-                const int have = __ldg(a.cache_lens + seq);
+                const int have = a.cache_lens[seq];
                 if (have < 0 || have + j > 0x7fffffff) seq = -1;   // an unused row of the batch
                 else pos = (int)(have + j);
             }
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) attn_append_kernel(const Ap
     const int pairs = a.rotary / 2;
     for (int i = tid; i < TOKENS * pairs; i += kAppendThreads) {
         const int tk = i / pairs, f = i - tk * pairs;
-        const double turns = (double)s_pos[tk] * (double)__ldg(a.inv_freq + f) * 0.15915494309189533577;   // / 2 pi
+        const double turns = (double)s_pos[tk] * (double)a.inv_freq[f] * 0.15915494309189533577;   // / 2 pi
         float s, c;
         sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
         s_turn[tk][f] = make_float2(c, s);
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) attn_append_kernel(const Ap
         }
         const int pos = s_pos[tk], col = pos >> a.cache.page_log2;
         int page = -1;
-        if (col < a.cache.width) page = __ldg(a.cache.table + seq * a.cache.row + col);
+        if (col < a.cache.width) page = a.cache.table[seq * a.cache.row + col];
         if (page < 0 || page >= a.cache.num_pages) {
             record_device_error(kDevErrBadPage);
             continue;

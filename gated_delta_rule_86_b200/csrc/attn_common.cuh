@@ -17,6 +17,8 @@ constexpr int kDevErrBadPage = 5;
 // runs (programmatic dependent launch): their blocks come up, set up what is theirs alone, and wait there for
 // the end of what is before them, ahead of their first access to memory.  A decode step's kernels are so
 // short that coming up is a third of their time.
+// What earlier kernels may have written is read by plain loads: the non-coherent ones (__ldg) are for data that no
+// one writes while a kernel is resident, which does not hold for a kernel that comes up under its writer.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -56,7 +58,7 @@ __device__ __forceinline__ void seq_range(const int32_t *cu, int n, int T, int64
         len = T;
         return;
     }
-    const int a = min(max(__ldg(cu + n), 0), T), b = min(max(__ldg(cu + n + 1), a), T);
+    const int a = min(max(cu[n], 0), T), b = min(max(cu[n + 1], a), T);
     first = a;
     len = b - a;
 }

@@ -18,6 +18,7 @@
 #pragma once
 
 #include "attn_common.cuh"
+#include "tc_utils.cuh"
 
 namespace kda {
 namespace attn {
@@ -48,21 +49,24 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
 }
 
 // Tokens of sequence b that there are: its length, at most what its row of the table can hold.
-__host__ __device__ __forceinline__ int decode_len(const DecodeArgs &a, int b) {
+__host__ __device__ __forceinline__ int clip_len(const DecodeArgs &a, int len) {
     const int64_t most = (int64_t)a.cache.width << a.cache.page_log2;
-    return (int)min((int64_t)max(a.lens[b], 0), most);
+    return (int)min((int64_t)max(len, 0), most);
+}
+__host__ __device__ __forceinline__ int decode_len(const DecodeArgs &a, int b) { return clip_len(a, a.lens[b]); }
+// The same ahead of a kernel's wait: at GPU scope, so that no line that an SM kept from before is taken for it.
+__device__ __forceinline__ int decode_len_early(const DecodeArgs &a, int b) {
+    return clip_len(a, tc::ld_relaxed_gpu(a.lens + b));
 }
 // What a pair costs beside its tiles (its queries, the join of the warps), in tiles: it counts in the shares,
 // or blocks with many short pairs would end long after the others.
 constexpr int kPairCost = 2;
-template <int TILE> __device__ __forceinline__ int decode_tiles(const DecodeArgs &a, int b) {
-    return (decode_len(a, b) + TILE - 1) / TILE;
-}
-
 // Length of a pair on the line.
+template <int TILE> __device__ __forceinline__ int units_of(int len) {
+    return len > 0 ? (len + TILE - 1) / TILE + kPairCost : 0;
+}
 template <int TILE> __device__ __forceinline__ int decode_units(const DecodeArgs &a, int b) {
-    const int t = decode_tiles<TILE>(a, b);
-    return t > 0 ? t + kPairCost : 0;
+    return units_of<TILE>(decode_len(a, b));
 }
 
 // Sum over the block; every thread gets it.
@@ -203,7 +207,7 @@ template <typename T, int D, int GC> __device__ __forceinline__ void write_empty
 
 // A sequence longer than its row of the table is cut there, and reported.
 __device__ __forceinline__ void check_len(const DecodeArgs &a, int b) {
-    if (__ldg(a.lens + b) > decode_len(a, b)) record_device_error(kDevErrBadPage);
+    if (a.lens[b] > decode_len(a, b)) record_device_error(kDevErrBadPage);
 }
 
 // Copies a warp's 16 tokens of the tile at `w` into its stage; returns a mask of the valid ones.
@@ -216,7 +220,7 @@ __device__ __forceinline__ uint32_t load_tokens(const DecodeArgs &a, const Walk<
     const int tok = t0 + (lane & 15);
     int page = -1;
     if (tok < w.len) {
-        page = __ldg(a.cache.table + w.b * a.cache.row + (tok >> a.cache.page_log2));
+        page = a.cache.table[w.b * a.cache.row + (tok >> a.cache.page_log2)];
         if (page < 0 || page >= a.cache.num_pages) {
             record_device_error(kDevErrBadPage);
             page = -1;
@@ -448,10 +452,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x / a.vheads, vh = blockIdx.x % a.vheads;
     next_may_start();
     // The lengths are older than the kernel before this one, which lets this one start when it has itself
-    // waited for them; so the shares are worked out while it runs.
+    // waited for them, so they are complete in memory; the shares are worked out while it runs.
     int64_t all = 0, before = 0;
     for (int n = tid; n < a.n; n += blockDim.x) {
-        const int t = decode_units<TILE>(a, n);
+        const int t = units_of<TILE>(decode_len_early(a, n));
         all += t;
         if (n < b) before += t;
     }
@@ -459,7 +463,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
     before = block_sum(before, scratch) * a.vheads;
     const int group = a.Hq / a.Hkv, chunks = a.vheads / a.Hkv, hkv = vh / chunks, h0 = hkv * group + (vh % chunks) * GC;
     const int nh = min(GC, hkv * group + group - h0);
-    const int tiles = decode_tiles<TILE>(a, b);
+    const int tiles = (decode_len_early(a, b) + TILE - 1) / TILE;
     const Shares sh(all, a.blocks);
     const int64_t s0 = before + (int64_t)vh * (tiles + kPairCost);
     const int c0 = tiles > 0 ? (int)sh.of(s0) : 0, c1 = tiles > 0 ? (int)sh.of(s0 + tiles - 1) : 0;

@@ -151,10 +151,10 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             const int c = kk * 8 + gc;
-            qf[kk][0] = gr < nh ? __ldg(q + gr * (D / 2) + c) : 0u;
-            qf[kk][2] = gr < nh ? __ldg(q + gr * (D / 2) + c + 4) : 0u;
-            qf[kk][1] = kBoth && gr + 8 < nh ? __ldg(q + (gr + 8) * (D / 2) + c) : 0u;
-            qf[kk][3] = kBoth && gr + 8 < nh ? __ldg(q + (gr + 8) * (D / 2) + c + 4) : 0u;
+            qf[kk][0] = gr < nh ? q[gr * (D / 2) + c] : 0u;
+            qf[kk][2] = gr < nh ? q[gr * (D / 2) + c + 4] : 0u;
+            qf[kk][1] = kBoth && gr + 8 < nh ? q[(gr + 8) * (D / 2) + c] : 0u;
+            qf[kk][3] = kBoth && gr + 8 < nh ? q[(gr + 8) * (D / 2) + c + 4] : 0u;
         }
     };
     load_q();

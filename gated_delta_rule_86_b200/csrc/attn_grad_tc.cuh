@@ -329,8 +329,8 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const bool there = r0 + e * 32 + lane < w.nq;
-                    ls[e] = there ? __ldg(a.lse + at + e * 32) : -CUDART_INF_F;
-                    de[e] = there ? __ldg(a.delta + at + e * 32) : 0.f;
+                    ls[e] = there ? a.lse[at + e * 32] : -CUDART_INF_F;
+                    de[e] = there ? a.delta[at + e * 32] : 0.f;
                 }
                 if ((r0 += kTile) >= w.nq) r0 = w.start * kTile, ++h;
             };
@@ -689,10 +689,9 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                 uint4 rest[D / 32];
 #pragma unroll
                 for (int y = 0; y < D / 32; ++y)
-                    rest[y] = a.rest && there ? __ldg(reinterpret_cast<const uint4 *>(
-                                                          static_cast<const __nv_bfloat16 *>(a.rest) +
-                                                          ((w.q0 + qi) * a.bt.Hq + w.head) * (int64_t)D) +
-                                                      part * (D / 32) + y)
+                    rest[y] = a.rest && there ? reinterpret_cast<const uint4 *>(
+                                                    static_cast<const __nv_bfloat16 *>(a.rest) +
+                                                    ((w.q0 + qi) * a.bt.Hq + w.head) * (int64_t)D)[part * (D / 32) + y]
                                               : make_uint4(0, 0, 0, 0);
                 ok = warp_wait(&bars.own_full, own & 1, abort) && R2::wait_full(bars, base + own);
                 if (!ok) break;

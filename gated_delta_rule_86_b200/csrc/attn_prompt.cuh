@@ -268,7 +268,7 @@ __device__ __forceinline__ void stage_stats(float *lse2, float *delta, const Pro
 // share, in 16-byte pieces (`row` elements each).
 template <typename T> __device__ __forceinline__ void zero_behind(T *g, const int32_t *cu, int n, int T_, int row) {
     if (cu == nullptr) return;
-    const int from = min(max(__ldg(cu + n), 0), T_);
+    const int from = min(max(cu[n], 0), T_);
     const int64_t pieces = (int64_t)(T_ - from) * row * (int)sizeof(T) / 16;
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, blocks = (int64_t)gridDim.x * gridDim.y;
     for (int64_t i = block * blockDim.x + threadIdx.x; i < pieces; i += blocks * blockDim.x)

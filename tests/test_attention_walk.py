@@ -1,5 +1,7 @@
-"""The bf16 decode step's walk over its tiles, run on the host from the kernel's own source (tests/csrc/attn_probe.cu)."""
+"""The attention kernels' source, and the bf16 decode step's walk over its tiles, run on the host from it
+(tests/csrc/attn_probe.cu)."""
 import ctypes
+import glob
 import os
 
 import pytest
@@ -46,3 +48,12 @@ def test_pages_are_looked_up_inside_the_table(probe, lens, page_log2, vheads, ga
                 assert hits(b, vh, t, warp) == 0
         for count in range(1, line + 1):   # shares of every length from the line's begin on
             assert hits(first, 0, count, warp) == 0
+
+
+def test_no_loads_that_promise_constant_data():
+    """The kernels come up while their inputs' writers still run, so none of their loads may be a non-coherent one."""
+    files = glob.glob(os.path.join(os.path.dirname(HERE), "gated_delta_rule_86_b200", "csrc", "attn_*.cuh"))
+    assert len(files) >= 8
+    for path in files:
+        code = "\n".join(line.split("//")[0] for line in open(path).read().splitlines())
+        assert "__ldg" not in code and "global.nc" not in code, path
