@@ -1,0 +1,147 @@
+"""Softmax attention on the GPU, on the paths that a call takes by its sizes: shares and join of the decode step, the
+large fp32 blocks, more than 128 packed sequences, appends of many tokens.  Bounds as in test_gpu_attention."""
+import pytest
+import torch
+
+import gated_delta_rule_86_b200 as kda
+from oracle import attention as ref
+from test_gpu_attention import (BF16, FP32, cache_of, check_append, check_decode, check_lse, decode_ref, inside, make,
+                                offsets)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _library(cuda_lib):
+    yield
+    torch.cuda.synchronize()
+    kda.device_error()
+
+
+# ---- decode: tables that hold more than a block takes by itself -----------------------------------
+
+LENS = [1500, 1, 0, 129, 3001, 2048, -2, 700]
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (2, 1), (4, 1), (6, 2), (8, 1), (16, 1), (20, 1), (24, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_decode_shares(hq, hkv, d, dtype):
+    kc, vc, table = cache_of(LENS, hkv, d, 64, dtype, 900, fill=float("nan"))
+    check_decode(make((len(LENS), hq, d), 910, dtype), kc, vc, table, LENS)
+    assert kda.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [1, 8, 16, 128])
+def test_decode_shares_pages(size, d, dtype):
+    lens = [1100, 77, 2049]
+    kc, vc, table = cache_of(lens, 2, d, size, dtype, 920)
+    check_decode(make((3, 8, d), 921, dtype), kc, vc, table, lens, scale=0.13)
+
+
+@pytest.mark.parametrize("d,hq", [(64, 4), (128, 4), (128, 16)])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_decode_shares_with_bad_pages_and_cut_lengths(dtype, d, hq):
+    lens = [1300, 2100]
+    kc, vc, table = cache_of(lens, 1, d, 32, dtype, 930)
+    q = make((2, hq, d), 931, dtype)
+    broken = table.clone()
+    gone = [[0, 7, 40], [3, 64, 65]]
+    for n, pages in enumerate(gone):
+        for page, bad in zip(pages, (-1, kc.shape[0], -2 ** 31)):
+            broken[n, page] = bad
+    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = kda.kda_attn_decode_step(q, kc, vc, broken, seq)
+    assert kda.device_error() == 5
+    for n in range(2):
+        keep = [p for p in range(lens[n]) if p // 32 not in gone[n]]
+        k, v = (ref.gather_cache(c, table[n], lens[n])[keep][None] for c in (kc, vc))
+        o, _, tol, _ = ref.attention(q[n:n + 1, None], k, v, causal=False)
+        inside(out[n], o[0, 0], tol[0, 0], "out")
+    # a length beyond the table's row counts as the row's
+    narrow = table[:, :40].contiguous()
+    out = kda.kda_attn_decode_step(q, kc, vc, narrow, seq)
+    assert kda.device_error() == 5
+    o, _, tol, _ = decode_ref(q, kc, vc, narrow, [1280, 1280])
+    inside(out, o[:, 0], tol[:, 0], "cut")
+
+
+def test_decode_shares_in_a_graph_with_lengths_that_it_moves():
+    """The lengths are changed by a kernel of the graph just before the step, whose second kernel reads them early."""
+    B, hq, hkv, d, size, steps = 5, 16, 2, 128, 16, 24
+    start = [1000, 120, 1270, 3, 2040]
+    kc, vc, table = cache_of([n + steps + 1 for n in start], hkv, d, size, BF16, 940)
+    q = make((B, hq, d), 941, BF16)
+    have = torch.tensor(start, dtype=torch.int32, device="cuda")
+    want = [kda.kda_attn_decode_step(q, kc, vc, table, have + i) for i in range(1, steps + 1)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        kda.kda_attn_decode_step(q, kc, vc, table, have)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        have.add_(1)
+        out = kda.kda_attn_decode_step(q, kc, vc, table, have)
+    got = []
+    for _ in range(steps):
+        graph.replay()
+        got.append(out.clone())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda.synchronize()
+
+
+# ---- prompts ------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_fp32_large_blocks(causal, d):
+    """As many blocks of 64 rows as there are SMs and more, dense and packed."""
+    for lens, B in ((None, 2), ([300, 0, 129, 571], 1)):
+        T = sum(lens) if lens else 500
+        q, k, v, g = (make((B, T, h, d), 960 + i, FP32) for i, h in enumerate((12, 12, 12, 12)))
+        cu = offsets(lens) if lens else None
+        out, lse = kda.kda_attn_fwd(q, k, v, cu, causal=causal, return_lse=True)
+        o, l, tol, ltol = ref.attention(q, k, v, cu, causal=causal)
+        inside(out, o, tol, "out")
+        check_lse(lse, l, ltol)
+        got = kda.kda_attn_bwd(q, k, v, out, lse, g, cu, causal=causal)
+        want, tols = ref.attention_grad(q, k, v, g, cu, causal=causal)
+        for x, y, t, name in zip(got, want, tols, ("dq", "dk", "dv")):
+            inside(x, y, t, name)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (BF16, 128), (FP32, 64)])
+@pytest.mark.parametrize("own_keys", [False, True])
+def test_prompt_more_than_128_sequences(own_keys, dtype, d):
+    """Sequences of several tiles among many short and empty ones, with keys of their own lengths or not."""
+    nq = [(11 * i) % 40 for i in range(150)]
+    for i, n in ((3, 300), (40, 129), (77, 513), (128, 256), (149, 400)):
+        nq[i] = n
+    nk = [(n + 17 * i) % 150 if i % 3 else n for i, n in enumerate(nq)] if own_keys else nq
+    if own_keys:
+        nk[77], nk[128] = 700, 100
+    q, k, v, g = (make((1, sum(n), h, d), 970 + i, dtype) for i, (n, h) in enumerate(((nq, 4), (nk, 2), (nk, 2), (nq, 4))))
+    cu, cu_k = offsets(nq), offsets(nk) if own_keys else None
+    out, lse = kda.kda_attn_fwd(q, k, v, cu, cu_k, return_lse=True)
+    o, l, tol, ltol = ref.attention(q, k, v, cu, cu_k)
+    inside(out, o, tol, "out")
+    check_lse(lse, l, ltol)
+    got = kda.kda_attn_bwd(q, k, v, out, lse, g, cu, cu_k)
+    want, tols = ref.attention_grad(q, k, v, g, cu, cu_k)
+    for x, y, t, name in zip(got, want, tols, ("dq", "dk", "dv")):
+        inside(x, y, t, name)
+
+
+# ---- append -------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("d,rotary,interleaved", [(64, 64, False), (128, 128, True), (128, 48, False), (64, 0, False)])
+def test_append_thousands_of_tokens(d, rotary, interleaved, dtype):
+    check_append([1300, 0, 5, 2200], [3, 9, 70, 0], 4, 2, d, 16, dtype, rotary, interleaved, seed=980)
+    check_append([650] * 3, [0, 31, 32], 3, 1, d, 32, dtype, rotary, interleaved, packed=False, seed=985)
+    assert kda.device_error() == 0
