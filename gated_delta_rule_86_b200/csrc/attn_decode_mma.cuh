@@ -6,7 +6,11 @@
 // loaded value and product: more than the FMA units give at the memory's pace, and little for m16n8k16
 // instructions.  Rows are the group's heads (up to 16), columns the warp's 16 tokens:
 //     S (16 x 16) = Q K^T      K straight from the staged rows
-//     O (16 x d) += P V        P from S's own registers, rounded to bf16, the operand type of V
+//     O (16 x d) += P V        P from S's own registers, as the sum of two bf16 numbers, the operand type of V:
+//                              the weight rounded, and what that took from it: good to 2^-16 of the weight, so only
+//                              the result's own rounding shows.  For up to 8 heads the second number takes the rows
+//                              that would be empty and costs nothing, for 16 a product of its own (heads of 128:
+//                              64 sequences of 4096 tokens 56.7 us, 56.6 without; 16 of 700 13.4 and 12.8).
 // tcgen05 would want 64 or 128 rows and its operands through Tensor Memory for the same few products;
 // the kernel is bound by the cache's bytes, not by these.
 // Measured, heads of 128, 4 query heads to one of the cache: 64 sequences of 64 to 16384 tokens 135 us, 6.2 TB/s;
@@ -36,6 +40,14 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// Two bf16 numbers in a word, and each of them as fp32.
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float low_half(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float high_half(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
 // The page of a warp's first token of a tile, -1 where it has none; its lookup runs a tile ahead of its use.
 template <int TILE>
@@ -195,54 +207,68 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
                 mma_bf16(s0, qf[kk], b[0], b[1]);
                 mma_bf16(s1, qf[kk], b[2], b[3]);
             }
-            uint32_t p[4] = {0u, 0u, 0u, 0u};
-            float f[2] = {1.f, 1.f};
-            bool any = false;
+            // scores in log2 units, row 8 y + gr, this lane's four tokens
+            constexpr int kRows = kBoth ? 2 : 1;
+            float x[kRows][4];
+            bool grow = false;
 #pragma unroll
-            for (int y = 0; y < (kBoth ? 2 : 1); ++y) {
-                float x[4] = {s0[2 * y], s0[2 * y + 1], s1[2 * y], s1[2 * y + 1]};
+            for (int y = 0; y < kRows; ++y) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] *= sc;
+                for (int e = 0; e < 4; ++e) x[y][e] = (e < 2 ? s0 : s1)[2 * y + (e & 1)] * sc;
                 if (ok != 0xffffu) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (!((ok >> (2 * gc + (e & 1) + (e >> 1) * 8)) & 1)) x[e] = -CUDART_INF_F;
+                        if (!((ok >> (2 * gc + (e & 1) + (e >> 1) * 8)) & 1)) x[y][e] = -CUDART_INF_F;
                 }
-                float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // the maximum in use follows the true one when it is 2^8 behind: weights up to 2^8 are as
-                // exact, and the accumulators are rescaled rarely
-                if (top - m[y] > 8.f) {
-                    f[y] = ex2_approx(m[y] - top);
-                    m[y] = top;
-                    any = true;
-                }
-                const float base = m[y] == -CUDART_INF_F ? 0.f : m[y];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = ex2_approx(x[e] - base);
-                l[y] = l[y] * f[y] + ((x[0] + x[1]) + (x[2] + x[3]));
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
-                p[y] = *reinterpret_cast<const uint32_t *>(&lo);
-                p[2 + y] = *reinterpret_cast<const uint32_t *>(&hi);
+                grow |= fmaxf(fmaxf(x[y][0], x[y][1]), fmaxf(x[y][2], x[y][3])) - m[y] > 8.f;
             }
-            if (__any_sync(0xffffffffu, any)) {
+            // the maximum in use follows the true one when it is 2^8 behind: weights up to 2^8 are as exact, and
+            // the lanes of a row exchange their maxima, and the accumulators are rescaled, rarely
+            if (__any_sync(0xffffffffu, grow)) {
+                float f[kRows];
+#pragma unroll
+                for (int y = 0; y < kRows; ++y) {
+                    float top = fmaxf(fmaxf(x[y][0], x[y][1]), fmaxf(x[y][2], x[y][3]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    f[y] = 1.f;
+                    if (top - m[y] > 8.f) {
+                        f[y] = ex2_approx(m[y] - top);
+                        m[y] = top;
+                    }
+                    l[y] *= f[y];
+                }
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
                     o[c][0] *= f[0];
                     o[c][1] *= f[0];
-                    if (kBoth) {
-                        o[c][2] *= f[1];
-                        o[c][3] *= f[1];
-                    }
+                    o[c][2] *= f[kRows - 1];
+                    o[c][3] *= f[kRows - 1];
                 }
             }
+            uint32_t p[4], pr[4];   // weights, and what rounding took from them
+#pragma unroll
+            for (int y = 0; y < kRows; ++y) {
+                const float base = m[y] == -CUDART_INF_F ? 0.f : m[y];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[y][e] = ex2_approx(x[y][e] - base);
+                l[y] += (x[y][0] + x[y][1]) + (x[y][2] + x[y][3]);
+                p[y] = pack_pair(x[y][0], x[y][1]);
+                p[2 + y] = pack_pair(x[y][2], x[y][3]);
+                pr[y] = pack_pair(x[y][0] - low_half(p[y]), x[y][1] - high_half(p[y]));
+                pr[2 + y] = pack_pair(x[y][2] - low_half(p[2 + y]), x[y][3] - high_half(p[2 + y]));
+            }
+            if (!kBoth) p[1] = pr[0], p[3] = pr[2];
 #pragma unroll
             for (int c2 = 0; c2 < D / 16; ++c2) {
                 uint32_t b[4];
                 ldsm4_t(b, ks + (vat ^ ((2 * c2 & 7) << 4)) + (c2 >> 2) * 128);
                 mma_bf16(o[2 * c2], p, b[0], b[1]);
                 mma_bf16(o[2 * c2 + 1], p, b[2], b[3]);
+                if (kBoth) {
+                    mma_bf16(o[2 * c2], pr, b[0], b[1]);
+                    mma_bf16(o[2 * c2 + 1], pr, b[2], b[3]);
+                }
             }
         }
         __syncwarp();   // the stage is read before it is filled again
@@ -273,7 +299,9 @@ __global__ void __launch_bounds__(DecodeMmaCfg<D, GC>::kWarps * 32, 1) attn_deco
                         float *j = s_join + ((warp % kPerRound) * GC + gr + 8 * y) * C::kPitch;
 #pragma unroll
                         for (int c = 0; c < D / 8; ++c)
-                            *reinterpret_cast<float2 *>(j + c * 8 + gc * 2) = make_float2(o[c][2 * y], o[c][2 * y + 1]);
+                            *reinterpret_cast<float2 *>(j + c * 8 + gc * 2) =
+                                kBoth ? make_float2(o[c][2 * y], o[c][2 * y + 1])
+                                      : make_float2(o[c][0] + o[c][2], o[c][1] + o[c][3]);
                         if (gc == 0) j[D] = m[y], j[D + 1] = l[y];
                     }
                 }

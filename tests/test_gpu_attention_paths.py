@@ -1,5 +1,7 @@
 """Softmax attention on the GPU, on the paths that a call takes by its sizes: shares and join of the decode step, the
 large fp32 blocks, more than 128 packed sequences, appends of many tokens.  Bounds as in test_gpu_attention."""
+import math
+
 import pytest
 import torch
 
@@ -91,6 +93,30 @@ def test_decode_shares_in_a_graph_with_lengths_that_it_moves():
         got.append(out.clone())
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,wide", [(4, False), (16, False), (4, True), (16, True)])
+def test_decode_weights_keep_their_bits(hq, wide, d):
+    """bf16 outputs off by their own rounding alone.  Queries and keys with one channel each that is not zero make the
+    scores exact, so a weight's error is that of its exponent (the scale's product and the subtraction of the maximum
+    round, 2 e each for |x| < 8 in log2 units: 32 e), of the power (2^-22 = 4 e, in the weight and in the sum), of the
+    sum (n e) and of its rounding to two bf16 numbers, 2^-16; the sum of n products may truncate, 2 n e."""
+    n, size = 40, 16
+    lens = [n, 7, n - 1] + ([2000] if wide else [])
+    kc, vc, table = cache_of(lens, 1, d, size, BF16, 950)
+    kc[..., 1:] = 0
+    q = torch.zeros((len(lens), hq, d), dtype=BF16, device="cuda")
+    q[..., 0] = make((len(lens), hq), 951, BF16)
+    kc[..., 0].clamp_(-2, 2)
+    q.clamp_(-2, 2)
+    out = kda.kda_attn_decode_step(q, kc, vc, table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    for b, length in enumerate(lens[:3]):
+        k, v = (ref.gather_cache(c, table[b], length)[:, 0].double() for c in (kc, vc))
+        p = torch.softmax(q[b].double() @ k.T / math.sqrt(d), 1)
+        want, mass = p @ v, p @ v.abs()
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -16 + (2 * (32 + 4) + 3 * length) * 2.0 ** -24) * mass
+        inside(out[b], want, 1.01 * tol, "out")
 
 
 # ---- prompts ------------------------------------------------------------------------------------
