@@ -361,20 +361,29 @@ inline int decode_group_chunk(int group, bool bf16) {
     return group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8;
 }
 
-// Short contexts of few pairs: a block takes a whole pair, which saves the join and its launch.  `tokens`:
-// what a row of the page table can hold.
-// Shares and whole pairs, heads of 128, one sequence and 4 heads of the cache: 7.3 and 4.9 us at 256 tokens,
-// 9.7 and 10.5 at 1024, 11.4 and 17.9 at 2048; 16 sequences and 8 heads: 10.3 and 5.6, 15.8 and 11.4, 29.3 and
-// 24.0 (pairs almost fill the SMs there, but only while their lengths are alike).
-constexpr int kPairTokens = 1024;
 inline int64_t decode_pairs(int64_t n, int Hq, int Hkv, bool bf16) {
     const int group = Hq / Hkv, gc = decode_group_chunk(group, bf16);
     return n * Hkv * ((group + gc - 1) / gc);
 }
-inline bool decode_per_pair(int64_t pairs, int64_t tokens, int sms) { return pairs <= sms && tokens <= kPairTokens; }
+
+// Short contexts of few pairs: a block takes a whole pair, which saves the join and its launch.  `tokens`:
+// what a row of the page table can hold.
+// Whole pairs and shares, us, full rows of the table, 4 query heads to one of the cache:
+//   bf16, heads of 128 (64):  1 pair, 768 tokens 8.9 and 9.3 (7.8 and 8.4), 1024 10.8 and 9.6 (9.4 and 8.7);
+//                             32 pairs, 1024 11.1 and 11.0 (9.7 and 9.8); 128 pairs, 1024 14.8 and 19.6 (10.6 and 15.0)
+//   fp32 (its block walks 64 tokens at a time, in 3.5 us for 128 tokens, so its shares pay sooner):
+//                             1 pair, 256 10.7 and 10.2 (8.6 and 9.3), 512 17.8 and 11.4 (14.1 and 10.0);
+//                             64 pairs, 256 11.6 and 13.7 (9.3 and 12.7), 512 19.0 and 17.9 (14.9 and 14.7);
+//                             128 pairs, 512 20.1 and 24.4 (20.3 and 20.1), 1024 34.3 and 38.4 (35.8 and 31.5)
+// Pairs that almost fill the SMs gain beyond these limits as well, but only while their lengths are alike.
+inline bool decode_per_pair(int64_t pairs, int64_t tokens, int d, bool bf16, int sms) {
+    if (pairs > sms) return false;
+    if (bf16) return tokens <= (8 * pairs <= sms ? 768 : 1024);
+    return tokens <= (4 * pairs <= 3 * sms ? 256 : d == 128 ? 1024 : 512);
+}
 
 inline size_t decode_workspace_bytes(int64_t n, int Hq, int Hkv, int d, int64_t tokens, bool bf16, int sms) {
-    if (decode_per_pair(decode_pairs(n, Hq, Hkv, bf16), tokens, sms)) return 0;
+    if (decode_per_pair(decode_pairs(n, Hq, Hkv, bf16), tokens, d, bf16, sms)) return 0;
     return (size_t)kMaxDecodeBlocks * 2 * decode_group_chunk(Hq / Hkv, bf16) * (d + 2) * 4;
 }
 
@@ -384,7 +393,7 @@ template <typename T, int D, int GC, typename C> cudaError_t launch_decode_g(voi
     if (e != cudaSuccess) return e;
     a.vheads = a.Hkv * ((a.Hq / a.Hkv + GC - 1) / GC);
     const int64_t pairs = (int64_t)a.n * a.vheads, tokens = (int64_t)a.cache.width << a.cache.page_log2;
-    a.per_pair = decode_per_pair(pairs, tokens, sms);
+    a.per_pair = decode_per_pair(pairs, tokens, D, sizeof(T) == 2, sms);
     a.blocks = a.per_pair ? (int)pairs : decode_blocks(a, C::kTile, sms);
     e = launch_behind(kern, (unsigned)a.blocks, threads, C::kSmem, st, a);
     if (e != cudaSuccess || a.per_pair) return e;

@@ -81,3 +81,8 @@ extern "C" int attn_probe_give_up(int quit, int d, const void *q, const void *k,
     if (cudaMemcpyToSymbol(kda::g_device_error, &none, sizeof(none)) != cudaSuccess) return -1;
     return word;
 }
+
+// Whether the decode step gives each pair a block of its own; on the host.
+extern "C" int attn_probe_per_pair(int64_t pairs, int64_t tokens, int d, int bf16, int sms) {
+    return decode_per_pair(pairs, tokens, d, bf16 != 0, sms);
+}
