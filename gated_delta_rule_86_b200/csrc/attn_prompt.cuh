@@ -459,8 +459,7 @@ __global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_grad_q_kernel(co
 }
 
 // Both for small batches, side by side: neither fills the GPU.  The first blocks take the keys.  B1 T256 H2 D64:
-// 29 us, 45 one after the other; T48 H4 D128 11 and 21; T1024 H2 D64 108 and 158; T1024 H8 D64, where either comes
-// near to filling it alone, 309 and 287.
+// 29 us, 45 one after the other; T48 H4 D128 11 and 21; T1024 H2 D64 108 and 158.  (grad_rows has the limit.)
 template <int D>
 __global__ void __launch_bounds__(RowsCfg<16>::kThreads) attn_grad_both_kernel(const PromptArgs a, int kv_blocks) {
     zero_behind(static_cast<float *>(a.dk), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
@@ -475,13 +474,42 @@ template <typename K> cudaError_t allow_smem(K kern, int bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// Rows of a block: 64, or 16 where blocks of 64 rows would not reach every SM (a tile's work is then
-// spread over four times the blocks, and each is done sooner).  16 against 64, heads of 64, forward and
-// gradient: T256 H2 14 and 43 against 23 and 72 us; T1024 H2 48 and 153 against 80 and 267; T1024 H8 (128 blocks)
-// 87 and 281 against 80 and 268; B4 T1024 H4 (256 blocks) 146 and 480 against 125 and 419.  (Gradients in two
-// launches, which attn_grad_both_kernel has improved on for 16 rows.)
-inline int prompt_rows(const int32_t *cu, int n, int T, int heads, int sms) {
-    return max_tiles(cu, n, T, 64) * heads < sms ? 16 : 64;
+// Rows of a block: 64, or 16 where blocks of 64 rows would leave SMs idle (a tile's work is then spread over
+// four times the blocks, each done sooner, and costs more in all).  What counts is work: tiles of 64 rows, each by
+// the quarters of its keys that it sees, a half under a causal mask (three quarters in short sequences).
+inline int seen_quarters(const PromptArgs &a) {
+    const int len = a.bt.cu_q ? a.bt.Tq / a.bt.n : a.bt.Tq;
+    return !a.causal || a.bt.Tk >= 2 * (int64_t)a.bt.Tq ? 4 : len >= 512 ? 2 : 3;
+}
+inline int64_t likely_tiles(const int32_t *cu, int n, int T) {   // packed: the last tile of a sequence is half full
+    return cu == nullptr ? max_tiles(cu, n, T, 64) : T / 64 + n / 2;
+}
+inline int64_t query_work(const PromptArgs &a) {
+    return seen_quarters(a) * likely_tiles(a.bt.cu_q, a.bt.n, a.bt.Tq) * a.bt.Hq;
+}
+inline int64_t key_work(const PromptArgs &a) {
+    return seen_quarters(a) * likely_tiles(a.bt.cu_k, a.bt.n, a.bt.Tk) * a.bt.Hkv;
+}
+// Forward, us with 16 and with 64 rows (H heads of their own keys; causal unless said otherwise).  Heads of 64:
+// T1024 H6 64 and 80, H8 81 and 80, T8192 H1 438 and 613, B4 T1024 H4 137 and 125; B8 T256 H4 29 and 23; not causal: T512
+// H8 34 and 42, T1024 H5 101 and 80.  Heads of 128: T1024 H5 127 and 142, H6 144 and 142, H8 178 and 142; B4 T256 H4
+// 36.8 and 38.7, B8 T256 H3 48 and 39; not causal: T512 H8 79 and 73, T1024 H8 304 and 142.
+inline int prompt_rows(const PromptArgs &a, int d, int sms) {
+    return 8 * query_work(a) < (int64_t)sms * (d == 64 ? 15 : 10) ? 16 : 64;
+}
+// Gradient: both halves in one launch of blocks of 16 rows, or one after the other.  In one launch, in two with 16 and
+// with 64 rows, us, as above.  Heads of 64: T1024 H4 160, 203, 272; T1024 H6 234, 222, 272; T1024 H8 309, 289, 273; T8192
+// H1 2197, 1539, 2115; B8 T256 H4 108, 95, 76; not causal: T512 H8 166, 111, 140, T1024 H8 589, 424, 272.  Heads of 128:
+// T1024 H8 423, 558, 495; B8 T256 H3 114, 147, 131, H4 147, 180, 132; not causal: T512 H8 227, 245, 246, T1024 H5 534, 713, 481.
+// Queries by 64 rows and keys by 16, B2 T1024 H16 of 2 heads of keys: 1172 (1195, 1255, 1502).
+struct GradRows {
+    bool one;   // one launch
+    int q, k;
+};
+inline GradRows grad_rows(const PromptArgs &a, int d, int sms) {
+    const int64_t q = query_work(a), k = key_work(a);
+    return {a.bt.Tq > 0 && a.bt.Tk > 0 && 10 * (q + k) < (int64_t)sms * (d == 64 ? 23 : 40), 8 * q < (int64_t)sms * 15 ? 16 : 64,
+            8 * k < (int64_t)sms * 15 ? 16 : 64};
 }
 
 template <int D, int ROWS> cudaError_t launch_prompt_rows(const PromptArgs &a, cudaStream_t st) {
@@ -495,8 +523,7 @@ template <int D, int ROWS> cudaError_t launch_prompt_rows(const PromptArgs &a, c
 
 template <int D> cudaError_t launch_prompt(const PromptArgs &a, int sms, cudaStream_t st) {
     if (a.bt.Tq == 0) return cudaSuccess;
-    return prompt_rows(a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq, sms) == 16 ? launch_prompt_rows<D, 16>(a, st)
-                                                                       : launch_prompt_rows<D, 64>(a, st);
+    return prompt_rows(a, D, sms) == 16 ? launch_prompt_rows<D, 16>(a, st) : launch_prompt_rows<D, 64>(a, st);
 }
 
 template <int D, int ROWS> cudaError_t launch_grad_kv(const PromptArgs &a, cudaStream_t st) {
@@ -517,9 +544,8 @@ template <int D, int ROWS> cudaError_t launch_grad_q(const PromptArgs &a, cudaSt
 }
 
 template <int D> cudaError_t launch_prompt_grad(const PromptArgs &a, int sms, cudaStream_t st) {
-    const int rows_q = prompt_rows(a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq, sms),
-              rows_k = prompt_rows(a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv, sms);
-    if (a.bt.Tq > 0 && a.bt.Tk > 0 && rows_q == 16 && rows_k == 16) {
+    const GradRows rows = grad_rows(a, D, sms);
+    if (rows.one) {
         constexpr int smem = PromptCfg<D>::smem(16, 2, 6);
         static_assert(smem <= 232448, "shared memory");
         const cudaError_t e = allow_smem(attn_grad_both_kernel<D>, smem);
@@ -531,8 +557,8 @@ template <int D> cudaError_t launch_prompt_grad(const PromptArgs &a, int sms, cu
     }
     cudaError_t e = cudaSuccess;
     if (a.bt.Tq > 0)   // first: it forms the delta that the other reads
-        e = rows_q == 16 ? launch_grad_q<D, 16>(a, st) : launch_grad_q<D, 64>(a, st);
-    if (e == cudaSuccess && a.bt.Tk > 0) e = rows_k == 16 ? launch_grad_kv<D, 16>(a, st) : launch_grad_kv<D, 64>(a, st);
+        e = rows.q == 16 ? launch_grad_q<D, 16>(a, st) : launch_grad_q<D, 64>(a, st);
+    if (e == cudaSuccess && a.bt.Tk > 0) e = rows.k == 16 ? launch_grad_kv<D, 16>(a, st) : launch_grad_kv<D, 64>(a, st);
     return e;
 }
 

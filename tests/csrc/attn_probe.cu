@@ -86,3 +86,21 @@ extern "C" int attn_probe_give_up(int quit, int d, const void *q, const void *k,
 extern "C" int attn_probe_per_pair(int64_t pairs, int64_t tokens, int d, int bf16, int sms) {
     return decode_per_pair(pairs, tokens, d, bf16 != 0, sms);
 }
+
+// The rows of a block that fp32 prompts get: forward, gradient in one launch or not, its queries', its keys'; on the host.
+extern "C" void attn_probe_rows(int d, int causal, int n, int Tq, int Tk, int Hq, int Hkv, int packed, int sms, int32_t *rows) {
+    PromptArgs a = {};
+    const int32_t offsets = 0;   // never looked into
+    a.bt.cu_q = a.bt.cu_k = packed ? &offsets : nullptr;
+    a.bt.n = n;
+    a.bt.Tq = Tq;
+    a.bt.Tk = Tk;
+    a.bt.Hq = Hq;
+    a.bt.Hkv = Hkv;
+    a.causal = causal != 0;
+    const GradRows g = grad_rows(a, d, sms);
+    rows[0] = prompt_rows(a, d, sms);
+    rows[1] = g.one;
+    rows[2] = g.q;
+    rows[3] = g.k;
+}
