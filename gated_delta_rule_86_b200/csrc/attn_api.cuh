@@ -166,9 +166,12 @@ kda_status kda_kv_append(const void *q, const void *k, const void *v, int64_t q_
     a.k_out = k_out;
     if (a.tokens == 0) return KDA_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int sms = kda::device_sm_count();
+    if (sms < 1) return KDA_ERR_CUDA;
     if (dtype == KDA_F32)
-        return status_of(d == 64 ? launch_append_d<float, 64>(a, st) : launch_append_d<float, 128>(a, st));
-    return status_of(d == 64 ? launch_append_d<__nv_bfloat16, 64>(a, st) : launch_append_d<__nv_bfloat16, 128>(a, st));
+        return status_of(d == 64 ? launch_append_d<float, 64>(a, sms, st) : launch_append_d<float, 128>(a, sms, st));
+    return status_of(d == 64 ? launch_append_d<__nv_bfloat16, 64>(a, sms, st)
+                             : launch_append_d<__nv_bfloat16, 128>(a, sms, st));
 }
 
 kda_status kda_attn_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int64_t max_tokens,

@@ -186,11 +186,11 @@ __global__ void __launch_bounds__(kAppendThreads, 6) attn_append_kernel(const Ap
     }
 }
 
-template <typename T, int D> cudaError_t launch_append_d(const AppendArgs &a, cudaStream_t st) {
-    // few tokens: one per block, so that they spread over the SMs; many: four, whose sines (up to 64 each)
+template <typename T, int D> cudaError_t launch_append_d(const AppendArgs &a, int sms, cudaStream_t st) {
+    // few tokens (8 an SM): one per block, so that they spread over the SMs; many: four, whose sines (up to 64 each)
     // keep all 256 threads busy at once.  One against four, 32 + 8 heads of 128: 3.3 and 5.7 us at 16 tokens,
     // 5.2 and 5.9 at 592, 8.4 and 11.7 at 1184, 15.2 and 12.9 at 2368, 98 and 77 at 16384.
-    if (a.tokens <= 148 * 8)
+    if (a.tokens <= (int64_t)sms * 8)
         return launch_behind(attn_append_kernel<T, D, 1>, (unsigned)a.tokens, kAppendThreads, 0, st, a);
     return launch_behind(attn_append_kernel<T, D, 4>, (unsigned)((a.tokens + 3) / 4), kAppendThreads, 0, st, a);
 }
