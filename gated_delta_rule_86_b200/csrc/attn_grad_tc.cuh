@@ -20,8 +20,8 @@
 // compute warps' (a wait behind products in flight returns only with them), 19 brings the queries' lse and
 // delta to the keys' kernel.  P and dS are rounded once, to bf16, as operands.
 //
-// Bound by the tensor pipe: B2 T4096, 16 heads of 128, 430 us, its seven products at 1.12 PFLOP/s (0.8 of what a
-// library product sustains); 6 packed documents, 16 + 4 heads of 64, 187 us, where P and dS take as long as
+// Bound by the turns that weights and products of one tile take (tensor pipe 52% of the cycles): B2 T4096, 16 heads of
+// 128, 430 us, its seven products at 1.12 PFLOP/s (0.8 of what a library product sustains); 6 packed documents, 16 + 4 heads of 64, 187 us, where P and dS take as long as
 // the products.  Powers on the FMA units, as the forward has them, change nothing here (442 to 453 us).
 //
 // delta is taken from O as it was before its rounding where the caller kept what the rounding took (`rest`):
@@ -253,7 +253,7 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
 
     next_may_start();
     const uint32_t tmem = grad_setup<D>(bars, {1, kAhead ? 16 : 17, 17, 19});
-    if (tid == 32) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&maps.g);
+    if (tid == 32 && a.bt.Tq > 0) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&maps.g);
     wait_for_previous();
     zero_behind(static_cast<__nv_bfloat16 *>(a.dk), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
     zero_behind(static_cast<__nv_bfloat16 *>(a.dv), a.bt.cu_k, a.bt.n, a.bt.Tk, a.bt.Hkv * D);
@@ -321,6 +321,7 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
         // -lse in log2 units, -inf (weight zero) where there is no query or it sees nothing; -delta.  Read a
         // turn before they are needed: the loads wait long behind the tiles' traffic.
         for (int r = 0; ok && (ok = take_item(bars, w, r, lane)) && w.total >= 0; ++r) {
+            if (w.total == 0) continue;
             const int64_t at0 = stat_at(a.bt, w.q0, 0);   // a head's rows of a sequence lie side by side
             float ls[4], de[4];
             int h = w.head * group, r0 = w.start * kTile;
@@ -334,7 +335,7 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
                 }
                 if ((r0 += kTile) >= w.nq) r0 = w.start * kTile, ++h;
             };
-            if (w.total > 0) fetch();
+            fetch();
             for (int it = 0; it < w.total; ++it, ++base) {
                 float l[4], d[4];
 #pragma unroll
@@ -528,7 +529,8 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
 
     next_may_start();
     const uint32_t tmem = grad_setup<D>(bars, {2, 17, 16, 18});
-    if (tid == 32) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&maps.g), prefetch_map(&maps.o);
+    if (tid == 32 && a.bt.Tk > 0)
+        prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&maps.g), prefetch_map(&maps.o);
     wait_for_previous();
     zero_behind(static_cast<__nv_bfloat16 *>(a.dq), a.bt.cu_q, a.bt.n, a.bt.Tq, a.bt.Hq * D);
 

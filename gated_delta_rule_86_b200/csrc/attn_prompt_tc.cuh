@@ -29,8 +29,9 @@
 // The ring of loads runs on from item to item, and an item's first products start under the end of the one
 // before: a block per item cost 7.5 us (d = 64) to 9 us (128) of coming up and running dry, as much as 5 turns.
 //
-// Bound by the tensor pipe and the powers together, which take about the same time at d = 128 and the powers
-// longer at 64.  One prompt of 16384 tokens, 32 heads of 128: 2.1 ms, 1.05 PFLOP/s of visible pairs (three
+// No unit is full (tensor pipe 55%, SFU 42%, issue slots 53% of the cycles at d = 128): a tile's softmax is a chain of
+// waits, and its products and powers, which take about the same time at d = 128 and the powers longer at 64, take turns
+// two tiles deep.  One prompt of 16384 tokens, 32 heads of 128: 2.1 ms, 1.05 PFLOP/s of visible pairs (three
 // quarters of what a library product sustains under the power limit); 8 packed prompts of 64 to 4096, heads of
 // 64: 243 us; 200 tokens: 11 us, of which a launch, one TMA round trip and two turns in a row.
 //
@@ -109,8 +110,8 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 }
 
 // 2^x of two numbers on the FMA units, for x <= 127: x = n + f with |f| <= 1/2, 2^f by the
-// polynomial of degree 5 with the least largest relative error (7.5e-8, found by exchange; 2.1e-7 as
-// evaluated, no more than the SFU's), n added to the exponent.  Below -126 it stays at 2^-126;
+// polynomial of degree 5 with the least largest relative error (found by exchange; 1.5e-7 with the coefficients
+// rounded to fp32, 2.1e-7 as evaluated, no more than the SFU's), n added to the exponent.  Below -126 it stays at 2^-126;
 // NaN gives the largest number, infinite once rounded to bf16.
 // The SFU gives 16 powers a clock and SM, so a tile of 128 x 128 weights takes as long as its two
 // products of depth 128; taking a part of the powers here shortens the longer of the two.
@@ -133,7 +134,8 @@ __device__ __forceinline__ float2 ex2_fma(float2 x) {
 }
 
 // Registers of a thread, moved between the warpgroups of a block after its launch: what one gives up
-// (kDown) another takes (kUp); 128 (2 kUp + kDown) may not exceed what the launch gave all three.
+// (kDown) others take (kUp each): four warpgroups of softmax take, the fifth gives, and 128 (4 kUp + kDown) may not
+// exceed what the launch gave all five.
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
@@ -329,7 +331,7 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     next_may_start();
-    if (tid == 32) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v);
+    if (tid == 32 && a.bt.Tk > 0) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v);
     if (warp == 16) {
         tc::tmem_alloc(&bars.tmem, 512);
         tc::tmem_relinquish();

@@ -380,5 +380,6 @@ def kda_chunk(q, k, v, log_alpha, beta, initial_state=None, cu_seqlens=None, chu
 
 
 def device_error() -> int:
-    """Sync the current stream and return-and-clear the device error word (KDA_OK or KDA_ERR_TIMEOUT)."""
+    """Sync the current stream and return-and-clear the device error word: KDA_OK, KDA_ERR_TIMEOUT (a wait ran out)
+    or KDA_ERR_BAD_PAGE (a page or length outside the cache); the larger where both were met."""
     return _lib.load().kda_get_last_device_error(_stream_handle())
