@@ -104,3 +104,19 @@ extern "C" void attn_probe_rows(int d, int causal, int n, int Tq, int Tk, int Hq
     rows[2] = g.q;
     rows[3] = g.k;
 }
+
+namespace {
+__global__ void powers(const float *x, float *y, int n) {   // n even
+    const int i = 2 * (blockIdx.x * blockDim.x + threadIdx.x);
+    if (i + 1 >= n) return;
+    const float2 p = ex2_fma(make_float2(x[i], x[i + 1]));
+    y[i] = p.x;
+    y[i + 1] = p.y;
+}
+}  // namespace
+
+// y[i] = 2^x[i] as the prompt kernel computes a part of its weights on the FMA units; n even.
+extern "C" int attn_probe_powers(const float *x, float *y, int n) {
+    powers<<<(n / 2 + 255) / 256, 256>>>(x, y, n);
+    return cudaDeviceSynchronize() == cudaSuccess ? 0 : -1;
+}

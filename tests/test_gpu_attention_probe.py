@@ -1,4 +1,5 @@
-"""The prompt kernel's failure path on the GPU, made to happen without a GPU fault.
+"""Parts of the prompt kernel on the GPU (tests/csrc/attn_probe.cu): its powers on the FMA units, and its failure path,
+made to happen without a GPU fault.
 
 Every wait of the kernel on a barrier of its block is bounded, but two softmax warps that share rows also meet at
 barriers that are not.  The probe (tests/csrc/attn_probe.cu) runs the kernel with one softmax warp giving up, as if
@@ -6,6 +7,7 @@ its wait had run out, at each place where it can; the other warp of the pair may
 return with the error recorded, and the next call must be right.
 """
 import ctypes
+import math
 import os
 import time
 
@@ -48,3 +50,21 @@ def test_a_warp_that_gives_up_ends_the_kernel(probe, place, d, hq, hkv):
         assert time.perf_counter() - t0 < 5
     assert run(-1) == 0
     assert torch.equal(out, want)
+
+
+def test_powers_on_the_fma_units(probe):
+    """2^x by the polynomial: its error as a function, 1.55e-7 (scanned in 64 bits), and the roundings of its six steps:
+    the last one 2^-24, the one before it times |f| <= 1/2 of a factor of 0.7 and so on, less than 2^-24 together."""
+    probe.attn_probe_powers.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32]
+    n = 1 << 20
+    x = torch.cat((torch.linspace(-1, 1, n, device="cuda"), torch.linspace(-125.9, 126.9, n, device="cuda"),
+                   torch.arange(-126, 127, device="cuda").float().repeat(2)))
+    y = torch.empty_like(x)
+    assert probe.attn_probe_powers(x.data_ptr(), y.data_ptr(), x.numel()) == 0
+    want = torch.exp2(x.double())
+    assert ((y.double() - want).abs() / want).max().item() <= 1.55e-7 + 2 * 2.0 ** -24
+    edge = torch.tensor([-126.0, -127.0, -1e30, -math.inf, math.nan, 0.0], device="cuda")
+    y = torch.empty_like(edge)
+    assert probe.attn_probe_powers(edge.data_ptr(), y.data_ptr(), edge.numel()) == 0
+    assert ((y[:4].double() / 2.0 ** -126 - 1).abs() <= 2.0 ** -22).all()   # stays where it is below -126
+    assert torch.isinf(y[4].bfloat16()) and abs(y[5].item() - 1) <= 2.0 ** -22
