@@ -271,12 +271,13 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
 
     if (warp == 17) {
         int put1 = 0, put2 = 0;   // loads under way
+        PlaceFrom from;
         for (int r = 0;; ++r) {
             // the first keys of a sequence are seen by the most queries: they go first
             int n, count, level;
             const int64_t index = item_index(r);
             w.total = -1;
-            if (place_of(a.bt.cu_k, a.bt.n, a.bt.Tk, kTile, index / a.bt.Hkv, lane, n, count, level)) {
+            if (place_of(a.bt.cu_k, a.bt.n, a.bt.Tk, kTile, index / a.bt.Hkv, lane, n, count, level, from)) {
                 const Seq s = seq_of(a.bt, n);
                 w.q0 = s.q0, w.k0 = s.k0, w.nq = s.nq, w.nk = s.nk;
                 w.head = (int)(index % a.bt.Hkv);
@@ -544,11 +545,12 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
 
     if (warp == 17) {
         int put1 = 0, put2 = 0;   // loads under way
+        PlaceFrom from;
         for (int r = 0;; ++r) {
             int n, count, level;
             const int64_t index = item_index(r);
             w.total = -1;
-            if (place_of(a.bt.cu_q, a.bt.n, a.bt.Tq, kTile, index / a.bt.Hq, lane, n, count, level)) {
+            if (place_of(a.bt.cu_q, a.bt.n, a.bt.Tq, kTile, index / a.bt.Hq, lane, n, count, level, from)) {
                 const Seq s = seq_of(a.bt, n);
                 w.q0 = s.q0, w.k0 = s.k0, w.nq = s.nq, w.nk = s.nk;
                 w.head = (int)(index % a.bt.Hq);

@@ -273,13 +273,13 @@ static_assert(sizeof(FwdBars) <= 512, "barriers");
 
 // A block's r-th item; a whole warp.  Blocks take items there and back, so that none has the largest of
 // every round.
-__device__ __forceinline__ TwoTiles item_of(const PromptArgs &a, int pair_heads, int r, int lane) {
+__device__ __forceinline__ TwoTiles item_of(const PromptArgs &a, int pair_heads, int r, int lane, PlaceFrom &from) {
     const int units = pair_heads ? a.bt.Hq / 2 : a.bt.Hq, rows = pair_heads ? kTile : 2 * kTile;
     const int64_t index = (int64_t)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     int n, count, level;
     TwoTiles w;
     w.both = -1;
-    if (!place_of(a.bt.cu_q, a.bt.n, a.bt.Tq, rows, index / units, lane, n, count, level)) return w;
+    if (!place_of(a.bt.cu_q, a.bt.n, a.bt.Tq, rows, index / units, lane, n, count, level, from)) return w;
     const Seq s = seq_of(a.bt, n);
     w.q0 = s.q0, w.k0 = s.k0, w.nq = s.nq, w.nk = s.nk;
     const int u = (int)(index % units), t = level - 1;
@@ -387,8 +387,9 @@ attn_prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
         };
         auto loaded = [&](int k) { return warp_wait(&bars.full[k % C::kStages], (k / C::kStages) & 1, abort); };
         if (warp == 19) {
+            PlaceFrom from;
             for (int r = 0;; ++r) {
-                const TwoTiles w = item_of(a, pair_heads, r, lane);
+                const TwoTiles w = item_of(a, pair_heads, r, lane, from);
                 if (r >= 2 && !warp_wait(&bars.item_empty[r & 1], ((r >> 1) - 1) & 1, abort)) break;
                 if (lane == 0) {
                     bars.item[r & 1] = w;
