@@ -8,7 +8,8 @@ device's current stream, whichever device is current.  A token tensor whose last
 two dimensions are dense and whose tokens lie an even distance apart (a slice
 of a fused projection, say) is read where it is; any other layout is copied
 first.  Wrong shapes raise ValueError, wrong types TypeError, and a non-OK
-status of the library :class:`KdaError`.
+status of the library :class:`KdaError`.  Gradients flow through
+:func:`kda_attn` alone; the results of the other calls are detached.
 """
 from __future__ import annotations
 
@@ -81,6 +82,7 @@ def kda_kv_append(k, v, k_cache, v_cache, page_table, cache_lens, inv_freq=None,
     (2i, 2i+1) when ``interleaved``, by position * inv_freq[i]; None: no rotation.  q_rotated is None
     without q and is written to ``q_out`` where given (it may be a contiguous q itself); k_rotated is None unless
     ``return_k``.  Tokens without a valid page are left out and :func:`device_error` reports it.
+    The call has no gradient, and warns where an input requires one.
     """
     return _native().kv_append(k, v, k_cache, v_cache, page_table, cache_lens, inv_freq, q, cu_seqlens, interleaved,
                                return_k, q_out)

@@ -303,6 +303,11 @@ std::pair<OptTensor, OptTensor> kv_append(const Tensor &k, const Tensor &v, cons
                                           const Tensor &page_table, const Tensor &cache_lens, const OptTensor &inv_freq,
                                           const OptTensor &q, const OptTensor &cu_seqlens, bool interleaved, bool return_k,
                                           const OptTensor &q_out) {
+    if (at::GradMode::is_enabled() && (k.requires_grad() || v.requires_grad() || (q && q->requires_grad())) &&
+        PyErr_WarnEx(PyExc_UserWarning,
+                     "kda_kv_append has no gradient: its results do not lead back to inputs that require one "
+                     "(call it under torch.no_grad() where that is meant)", 1) != 0)
+        throw py::error_already_set();   // where warnings are errors
     if (k.dim() != 4 || v.sizes() != k.sizes()) bad_value("k and v must be [B, T, Hkv, d]");
     const int32_t B = i32(k.size(0)), T = i32(k.size(1)), Hkv = i32(k.size(2)), d = i32(k.size(3));
     const int64_t n = cu_seqlens ? cu_seqlens->numel() - 1 : B;

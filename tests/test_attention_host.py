@@ -1,5 +1,6 @@
 """Softmax attention without a GPU: what the calls refuse, on the host, before anything is launched."""
 import ctypes
+import warnings
 
 import pytest
 import torch
@@ -202,3 +203,19 @@ def test_forward_mode_is_refused(lib):
                 args[(i + 1) % 3] = plain.clone().requires_grad_(wants)
                 with pytest.raises(NotImplementedError, match="forward-mode"):
                     kda.kda_attn(*args)
+
+
+def test_append_says_that_it_has_no_gradient(lib):
+    x, i, t, c = torch.zeros(1, 1, 2, 64), torch.zeros(1, dtype=torch.int32), torch.zeros(1, 4, dtype=torch.int32), torch.zeros(4, 2, 16, 64)
+    leaf = x.clone().requires_grad_()
+    for k, q in ((leaf, None), (x, leaf)):
+        with pytest.warns(UserWarning, match="no gradient"), pytest.raises(ValueError, match="CUDA"):
+            kda.kda_kv_append(k, x, c, c, t, i, q=q)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(UserWarning, match="no gradient"):
+            kda.kda_kv_append(leaf, x, c, c, t, i)
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            kda.kda_kv_append(leaf, x, c, c, t, i)
+        with pytest.raises(ValueError, match="CUDA"):
+            kda.kda_kv_append(x, x, c, c, t, i, q=x)
