@@ -61,14 +61,21 @@ def build_binding(force: bool = False) -> str:
     from torch.utils.cpp_extension import include_paths
 
     src = os.path.join(HERE, "csrc", "attn_binding.cpp")
-    if not (force or _stale(BINDING_PATH, [src, os.path.join(ROOT, "include", "kda.h")])):
+    made_for = f"built for torch {torch.__version__}"   # it uses torch's internals, which change between versions
+
+    def other_torch():
+        with open(BINDING_PATH, "rb") as f:
+            return made_for.encode() + b"\0" not in f.read()
+
+    if not (force or _stale(BINDING_PATH, [src, os.path.join(ROOT, "include", "kda.h")]) or other_torch()):
         return BINDING_PATH
     build_library()
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DTORCH_API_INCLUDE_EXTENSION_H",
-           "-DTORCH_EXTENSION_NAME=_attention", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+           "-DTORCH_EXTENSION_NAME=_attention", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DKDA_BUILT_FOR="{made_for}"']
     for d in include_paths() + [os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]:
         cmd += ["-isystem", d]
     cmd += [src, "-o", tmp, f"-L{libs}", f"-L{HERE}", "-l:libkda_b200.so", "-ltorch_python", "-ltorch", "-ltorch_cpu",

@@ -427,4 +427,5 @@ PYBIND11_MODULE(_attention, m) {
         return py::cast(o);
     });
     m.def("tokens", &tokens);
+    m.attr("built_for") = KDA_BUILT_FOR;   // read from the file by the build
 }

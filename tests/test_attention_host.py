@@ -219,3 +219,17 @@ def test_append_says_that_it_has_no_gradient(lib):
             kda.kda_kv_append(leaf, x, c, c, t, i)
         with pytest.raises(ValueError, match="CUDA"):
             kda.kda_kv_append(x, x, c, c, t, i, q=x)
+
+
+def test_binding_is_built_again_for_another_torch(lib, monkeypatch):
+    from gated_delta_rule_86_b200 import build
+    assert _native().built_for == f"built for torch {torch.__version__}"
+    commands = []
+    monkeypatch.setattr(build.subprocess, "check_call", commands.append)
+    monkeypatch.setattr(build.os, "replace", lambda a, b: None)
+    build.build_binding()
+    assert not commands
+    for other in (torch.__version__ + "1", torch.__version__[:-1], "1.0"):
+        monkeypatch.setattr(torch, "__version__", other)
+        build.build_binding()
+        assert any(f"built for torch {other}" in str(x) for x in commands.pop())
