@@ -18,11 +18,11 @@
 // (thread = row, four groups of 32 columns), 16 issues the products, 17 finds the items and loads their tiles
 // (TMA), 18 waits for the loads on 16's behalf, zeroes rows that must not count, and joins its word to the
 // compute warps' (a wait behind products in flight returns only with them), 19 brings the queries' lse and
-// delta to the keys' kernel.  P and dS are rounded once, to bf16, as operands.
+// delta to the keys' kernel.  P and dS become operands in bf16 (see kFineKeys).
 //
 // Bound by the turns that weights and products of one tile take (tensor pipe 52% of the cycles): B2 T4096, 16 heads of
-// 128, 430 us, its seven products at 1.12 PFLOP/s (0.8 of what a library product sustains); 6 packed documents, 16 + 4 heads of 64, 187 us, where P and dS take as long as
-// the products.  Powers on the FMA units, as the forward has them, change nothing here (442 to 453 us).
+// 128, 433 us, its seven products at 1.11 PFLOP/s (0.8 of what a library product sustains); 6 packed documents,
+// 16 + 4 heads of 64, 191 us, where P and dS take as long as the products.  Powers on the FMA units, as the forward has them, change nothing here (442 to 453 us).
 //
 // delta is taken from O as it was before its rounding where the caller kept what the rounding took (`rest`):
 // delta is subtracted from every dP of its row, so the rounding's error in it (2^-9 |dO| |O|) does not cancel
@@ -60,7 +60,16 @@ struct GradItem {
     int64_t q0, k0;                            // the sequence's first query and key
     int nq, nk, total;                         // total: turns; -1: no more items
     int head, row0, start, per_head;           // keys' kernel: first query tile, turns per query head
+    int fine;                                  // operands as two numbers: keys' kernel: in so many turns at a head's begin
 };
+
+// P and dS enter their products rounded to bf16, or, where a tile of queries sees one tile of keys or less, as two
+// bf16 numbers, the second what rounding took from the first.  Among many keys the roundings' errors average out: they
+// add as much to the result's error as its own rounding does, 1.41 times that in all.  Queries that see a few have few
+// weights and the largest dS of their sequence: rounded, they make it 2.2 times for 2 tokens, 1.6 for 64, and still 1.5
+// for a causal sequence of 2048; as two numbers 1.3, 1.1 and 1.3.  Costs: 64 sequences of 64 tokens 72 us from 63, 16 of
+// 1024 240 from 237 (16 + 4 heads of 64), B2 T4096 H16 433 from 427; everywhere it would be 505.
+constexpr int kFineKeys = kTile;
 
 struct GradBars {
     uint64_t own_full, own_empty, out_read, first, full[8], empty[8], stats[2], stats_read[2], s_full[2], dp_full[2], q_word,
@@ -189,12 +198,18 @@ __device__ __forceinline__ int64_t item_index(int r) {
 }
 
 // 32 numbers of a thread's row, rounded, into Tensor Memory as an operand, over the first 16 columns of
-// the 32 that they were read from.
-__device__ __forceinline__ void put_operand(uint32_t taddr, const float2 (&x)[16]) {
+// the 32 that they were read from; FINE: and what rounding took from them over the other 16.
+template <bool FINE> __device__ __forceinline__ void put_operand(uint32_t taddr, const float2 (&x)[16]) {
     uint32_t u[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) u[e] = pack_bf16(x[e].x, x[e].y);
     tc::tmem_st16(taddr, u);
+    if constexpr (FINE) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            u[e] = pack_bf16(x[e].x - __uint_as_float(u[e] << 16), x[e].y - __uint_as_float(u[e] & 0xffff0000u));
+        tc::tmem_st16(taddr + 16, u);
+    }
 }
 // d (+)= x y with x such an operand of 128 columns, y an MN-major tile.
 __device__ __forceinline__ void chain_ts32(uint32_t d, uint32_t x, uint64_t y, uint32_t idesc, bool accumulate,
@@ -285,6 +300,9 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
                 w.start = a.causal ? max(0, w.row0 - (s.nk - s.nq)) / kTile : 0;   // query i sees keys j <= i + nk - nq
                 w.per_head = max(0, (s.nq + kTile - 1) / kTile - w.start);
                 w.total = w.per_head * group;
+                // tile t of the queries sees (t + 1) kTile + nk - nq keys
+                w.fine = s.nk <= kFineKeys ? w.per_head
+                         : a.causal ? min(w.per_head, max(0, (kFineKeys - (s.nk - s.nq)) / kTile - w.start)) : 0;
             }
             if (!(ok = give_item(bars, w, r, lane)) || w.total < 0) break;
             if (w.total == 0) continue;
@@ -396,8 +414,9 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
             if (!ok) break;
             scores(base, st1);
             products(base, st2, total == 1);
-            for (int it = 0; it < total; ++it, ++base) {
-                const bool more = it + 1 < total;
+            for (int it = 0, of_head = 0; it < total; ++it, ++base) {
+                const bool more = it + 1 < total, fine = of_head < w.fine;
+                if (++of_head == w.per_head) of_head = 0;
                 const int next1 = R1::after(st1), next2 = R2::after(st2);
                 const uint64_t q = desc_mn(sbase + R1::at(st1), 0), g = desc_mn(sbase + R2::at(st2), 0);
                 if (kAhead && more) {
@@ -408,11 +427,13 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
                 if (!(ok = wait_turn(bars.a_ready, base, abort))) break;
                 tc::tc_fence_after();
                 chain_ts32(tV, tS(base), g, idG, it > 0, leader);
+                if (fine) chain_ts32(tV, tS(base) + 16, g, idG, true, leader);
                 if (!kAhead && more) scores(base + 1, next1);
                 commit_by(&bars.empty[R2::bar(st2)], leader);
                 if (!(ok = wait_turn(bars.b_ready, base, abort))) break;
                 tc::tc_fence_after();
                 chain_ts32(tK, tP, q, idG, it > 0, leader);
+                if (fine) chain_ts32(tK, tP + 16, q, idG, true, leader);
                 if (more) products(base + 1, next2, it + 2 == total);
                 commit_by(&bars.empty[R1::bar(st1)], leader);
                 if (!more) commit_by(&bars.done, leader);
@@ -437,7 +458,8 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
             // this row's key is seen from this query on (where masked), and by the warp's rows all
             const int sees = a.causal ? w.row0 + row - (w.nk - nq) : INT_MIN / 2, all_see = sees + 31 - lane;
             int r0 = begin;
-            for (int it = 0; it < total; ++it, ++base) {
+            auto turns = [&](auto fine, int number) {   // once for either kind of operands: a test in each turn costs 4%
+            for (int it = 0; it < number; ++it, ++base) {
                 const float *ls = stats + (base & 1) * 2 * kTile + part * 32, *de = ls + kTile;
                 const int from = sees - r0 - part * 32;   // hidden columns before it
                 const bool partly = all_see - r0 - part * 32 > 0;
@@ -466,7 +488,7 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
                         if (2 * e + 1 < from) p[e].y = 0.f;
                     }
                 }
-                put_operand(tS(base) + lanes, p);
+                put_operand<decltype(fine)::value>(tS(base) + lanes, p);
                 arrive_operand(&bars.a_ready[base & 1], lane);
                 ok = wait_turn(bars.dp_full, base, abort);
                 if (!ok) break;
@@ -489,9 +511,14 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
                         if (2 * e + 1 < from) p[e].y = 0.f;
                     }
                 }
-                put_operand(tP + lanes, p);
+                put_operand<decltype(fine)::value>(tP + lanes, p);
                 arrive_operand(&bars.b_ready[base & 1], lane);
                 if (lane == 0) tc::mbar_arrive(&bars.stats_read[base & 1]);
+            }
+            };
+            for (int left = total; ok && left > 0; left -= w.per_head) {   // the group's heads
+                turns(std::true_type(), w.fine);
+                if (ok) turns(std::false_type(), w.per_head - w.fine);
             }
             if (ok && total > 0) ok = warp_wait(&bars.done, own++ & 1, abort);
             if (!ok) break;
@@ -556,6 +583,7 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                 w.head = (int)(index % a.bt.Hq);
                 w.row0 = (level - 1) * kTile;
                 w.total = (keys_seen(s, min(w.row0 + kTile, s.nq) - 1, a.causal) + kTile - 1) / kTile;
+                w.fine = w.total <= kFineKeys / kTile;
             }
             if (!(ok = give_item(bars, w, r, lane)) || w.total < 0) break;
             if (w.total == 0) continue;
@@ -651,6 +679,7 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                 if (!(ok = wait_turn(bars.b_ready, base, abort))) break;
                 tc::tc_fence_after();
                 chain_ts32(tQ, tP + (base & 1) * kTile, k, idG, j > 0, leader);
+                if (w.fine) chain_ts32(tQ, tP + (base & 1) * kTile + 16, k, idG, true, leader);
                 commit_by(&bars.empty[R1::bar(st1)], leader);
                 if (j + 1 == total) commit_by(&bars.done, leader);
                 st1 = next1;
@@ -722,6 +751,7 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
             }
             if (part == 0 && there) a.delta[at] = de;
             const float2 ls2 = make_float2(ls, ls), de2 = make_float2(-de, -de);
+            auto turns = [&](auto fine) {
             for (int j = 0; j < total; ++j, ++base) {
                 const uint32_t dp = tP + (base & 1) * kTile + lanes;
                 const int limit = seen - j * kTile - part * 32;   // columns at or past it are hidden
@@ -757,9 +787,12 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                         if (2 * e + 1 >= limit) p[e].y = 0.f;
                     }
                 }
-                put_operand(dp, p);
+                put_operand<decltype(fine)::value>(dp, p);
                 arrive_operand(&bars.b_ready[base & 1], lane);
             }
+            };
+            if (w.fine) turns(std::true_type());
+            else turns(std::false_type());
             if (ok && total > 0) ok = warp_wait(&bars.done, own++ & 1, abort);
             if (!ok) break;
             tc::tc_fence_after();
