@@ -96,9 +96,17 @@ __device__ __forceinline__ void dot_rows(float (&acc)[RPT][4], const float *A, c
     }
 }
 
-// acc[i][c] += sum_t W[RPT ty + i][t] X[t][channel c of tx]  (W pitch 68, X pitch D + 4)
-template <int D, int RPT>
+// acc[i][c] += sum_t W[RPT ty + i][t] X[t][channel c of tx]  (W pitch 68, X pitch D + 4).  APART: a tile's 64 products
+// are summed by themselves first, since one sum over all tiles errs as the root of all its terms: dK over 16 heads of
+// 1024 queries by 2.3e-6 of its size, and 4.5e-7 so.  It is free but for blocks of 16 rows (forward, heads of 128, 10%;
+// dQ, 5%), which have the fewest terms and do without it where they sum over keys alone.
+template <bool APART, int D, int RPT>
 __device__ __forceinline__ void weigh_rows(float (&acc)[RPT][D / 16], const float *W, const float *X, int ty, int tx) {
+    float tile[RPT][D / 16] = {};
+    auto &sum = *[&] {
+        if constexpr (APART) return &tile;
+        else return &acc;
+    }();
 #pragma unroll 2
     for (int t = 0; t < kPT; t += 4) {
         float4 w[RPT];
@@ -116,10 +124,15 @@ __device__ __forceinline__ void weigh_rows(float (&acc)[RPT][D / 16], const floa
             for (int i = 0; i < RPT; ++i) {
                 const float wi = u == 0 ? w[i].x : u == 1 ? w[i].y : u == 2 ? w[i].z : w[i].w;
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) acc[i][c] += wi * x[c];
+                for (int c = 0; c < D / 16; ++c) sum[i][c] += wi * x[c];
             }
         }
     }
+    if constexpr (APART)
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) acc[i][c] += tile[i][c];
 }
 
 // A thread's channels of one row: tx * 4 + {0 .. 3}, + 64 for the second four.
@@ -211,7 +224,7 @@ __global__ void __launch_bounds__(RowsCfg<ROWS>::kThreads) attn_prompt_kernel(co
             for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
         }
         put_weights(sp, x, ty, tx);
-        weigh_rows<D, RPT>(o, sp, ring + (2 * at + 1) * C::kTileF, ty, tx);
+        weigh_rows<ROWS == 64, D, RPT>(o, sp, ring + (2 * at + 1) * C::kTileF, ty, tx);
     }
     copies_wait();
 #pragma unroll
@@ -347,9 +360,9 @@ __device__ __forceinline__ void grad_kv(const PromptArgs &a, int64_t index, int 
         if (OWN_DELTA) __syncthreads();
         grad_scores(x, y, s, stats + 2 * at * kPT, stats + (2 * at + 1) * kPT, r0, c0, ty, tx, a.causal, true);
         put_weights(sp, x, ty, tx);
-        weigh_rows<D, RPT>(gv, sp, sg, ty, tx);
+        weigh_rows<true, D, RPT>(gv, sp, sg, ty, tx);
         put_weights(sp, y, ty, tx);
-        weigh_rows<D, RPT>(gk, sp, sq, ty, tx);
+        weigh_rows<true, D, RPT>(gk, sp, sq, ty, tx);
     }
     copies_wait();
 #pragma unroll
@@ -442,7 +455,7 @@ template <int D, int ROWS> __device__ __forceinline__ void grad_q(const PromptAr
             for (int j = 0; j < 4; ++j) x[i][j] *= sc;
         grad_scores(x, y, s, stats, stats + kPT, r0, c0, ty, tx, a.causal, false);
         put_weights(sp, y, ty, tx);
-        weigh_rows<D, RPT>(gq, sp, sk, ty, tx);
+        weigh_rows<ROWS == 64, D, RPT>(gq, sp, sk, ty, tx);
     }
     copies_wait();
 #pragma unroll

@@ -179,6 +179,20 @@ def test_gradient_of_few_keys_keeps_its_bits(T, limit, hq, hkv, d):
         assert (x.double() - w).norm().item() <= limit * least, name
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_gradient_fp32_of_many_terms(causal, d):
+    """dK and dV over 16 heads of 1024 queries.  A sum of n terms one after another errs by some sqrt(n) / 2 half steps
+    of 2^-24 of a random sum's size: sqrt(16384) / 2 = 64 of them in one go, (sqrt(64) + sqrt(256)) / 2 = 12 by tiles of 64;
+    8 more for scores, powers and dP."""
+    q, k, v, g = (make((1, 1024, h, d), 990 + i, FP32) for i, h in enumerate((16, 1, 1, 16)))
+    out, lse = kda.kda_attn_fwd(q, k, v, causal=causal, return_lse=True)
+    got = kda.kda_attn_bwd(q, k, v, out, lse, g, causal=causal)
+    want, _ = ref.attention_grad(q, k, v, g, causal=causal)
+    for x, w, name in zip(got, want, ("dq", "dk", "dv")):
+        assert (x.double() - w).norm() <= 20 * 2.0 ** -24 * w.norm(), name
+
+
 # ---- append -------------------------------------------------------------------------------------
 
 
