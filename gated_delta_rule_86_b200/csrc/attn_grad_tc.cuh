@@ -63,7 +63,7 @@ struct GradItem {
     int fine;                                  // operands as two numbers: keys' kernel: in so many turns at a head's begin
 };
 
-// P and dS enter their products rounded to bf16, or, where a tile of queries sees one tile of keys or less, as two
+// P and dS enter their products rounded to bf16, or, where the first of a tile of queries sees kFineKeys or less, as two
 // bf16 numbers, the second what rounding took from the first.  Among many keys the roundings' errors average out: they
 // add as much to the result's error as its own rounding does, 1.41 times that in all.  Queries that see a few have few
 // weights and the largest dS of their sequence: rounded, they make it 2.2 times for 2 tokens, 1.6 for 64, and still 1.5
@@ -300,9 +300,9 @@ attn_grad_kv_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_consta
                 w.start = a.causal ? max(0, w.row0 - (s.nk - s.nq)) / kTile : 0;   // query i sees keys j <= i + nk - nq
                 w.per_head = max(0, (s.nq + kTile - 1) / kTile - w.start);
                 w.total = w.per_head * group;
-                // tile t of the queries sees (t + 1) kTile + nk - nq keys
+                // the first query of tile t sees t kTile + 1 + nk - nq keys
                 w.fine = s.nk <= kFineKeys ? w.per_head
-                         : a.causal ? min(w.per_head, max(0, (kFineKeys - (s.nk - s.nq)) / kTile - w.start)) : 0;
+                         : a.causal ? min(w.per_head, max(0, (kFineKeys - (s.nk - s.nq) + kTile - 1) / kTile - w.start)) : 0;
             }
             if (!(ok = give_item(bars, w, r, lane)) || w.total < 0) break;
             if (w.total == 0) continue;
@@ -583,7 +583,7 @@ attn_grad_q_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constan
                 w.head = (int)(index % a.bt.Hq);
                 w.row0 = (level - 1) * kTile;
                 w.total = (keys_seen(s, min(w.row0 + kTile, s.nq) - 1, a.causal) + kTile - 1) / kTile;
-                w.fine = w.total <= kFineKeys / kTile;
+                w.fine = keys_seen(s, w.row0, a.causal) <= kFineKeys;
             }
             if (!(ok = give_item(bars, w, r, lane)) || w.total < 0) break;
             if (w.total == 0) continue;

@@ -163,14 +163,15 @@ def test_prompt_more_than_128_sequences(own_keys, dtype, d):
 
 
 @pytest.mark.parametrize("hq,hkv,d", [(1, 1, 64), (3, 1, 64), (2, 2, 128), (8, 2, 128)])
-@pytest.mark.parametrize("T,limit", [(9, 1.25), (20, 1.25), (64, 1.25), (128, 1.25), (1024, math.sqrt(2))])
-def test_gradient_of_few_keys_keeps_its_bits(T, limit, hq, hkv, d):
-    """The error of bf16 gradients, against that of the formula's gradient rounded to bf16, which is the least.  Up to a
-    tile of keys what is left comes through delta: the forward's weights are rounded, in an output that averages over
-    the keys, so at most half of a rounding's energy: sqrt(1 + 1/2).  Beyond, the rounding of the weights and of dS adds
-    one rounding's energy at most, sqrt(1 + 1)."""
+@pytest.mark.parametrize("T,past,limit", [(9, 0, 1.25), (20, 0, 1.25), (64, 0, 1.25), (128, 0, 1.25), (128, 1, 1.25), (70, 90, 1.25),
+                                          (1024, 0, math.sqrt(2)), (900, 7, math.sqrt(2))])
+def test_gradient_of_few_keys_keeps_its_bits(T, past, limit, hq, hkv, d):
+    """The error of bf16 gradients, against that of the formula's gradient rounded to bf16, which is the least.  Where the
+    first query of each tile sees a tile of keys at most, what is left comes through delta: the forward's weights are
+    rounded, in an output that averages over the keys, so at most half of a rounding's energy: sqrt(1 + 1/2).  Beyond,
+    the rounding of the weights and of dS adds one rounding's energy at most, sqrt(1 + 1)."""
     B = 1 if T > 128 else 16
-    q, k, v, g = (make((B, T, h, d), 975 + i, BF16) for i, h in enumerate((hq, hkv, hkv, hq)))
+    q, k, v, g = (make((B, t, h, d), 975 + i, BF16) for i, (t, h) in enumerate(((T, hq), (T + past, hkv), (T + past, hkv), (T, hq))))
     leaves = [t.requires_grad_() for t in (q, k, v)]
     got = torch.autograd.grad(kda.kda_attn(*leaves), leaves, g)
     want, _ = ref.attention_grad(*(t.detach() for t in (q, k, v)), g)
