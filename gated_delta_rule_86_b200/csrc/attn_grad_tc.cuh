@@ -20,13 +20,15 @@
 // compute warps' (a wait behind products in flight returns only with them), 19 brings the queries' lse and
 // delta to the keys' kernel.  P and dS become operands in bf16 (see kFineKeys).
 //
-// Bound by the turns that weights and products of one tile take (tensor pipe 52% of the cycles): B2 T4096, 16 heads of
-// 128, 433 us, its seven products at 1.11 PFLOP/s (0.8 of what a library product sustains); 6 packed documents,
-// 16 + 4 heads of 64, 191 us, where P and dS take as long as the products.  Powers on the FMA units, as the forward has them, change nothing here (442 to 453 us).
+// Bound by the turns that weights and products of one tile take (tensor pipe 55 to 59% of the cycles): B2 T4096, 16 heads of
+// 128, 427 us, its seven products at 1.13 PFLOP/s (0.8 of what a library product sustains); 6 packed documents,
+// 16 + 4 heads of 64, 190 us, where P and dS take as long as the products.  Powers on the FMA units, as the forward has
+// them, change nothing here.
 //
 // delta is taken from O as it was before its rounding where the caller kept what the rounding took (`rest`):
 // delta is subtracted from every dP of its row, so the rounding's error in it (2^-9 |dO| |O|) does not cancel
-// in the sum.  dQ's error against 64 bits is 2.4e-3 of its size with it, 2.5 to 2.9e-3 without; 1 us.
+// in the sum.  dQ's error against 64 bits is 1.74e-3 of its size with it, 2.04e-3 without, for 64 tokens, 2.06 and
+// 2.20e-3 for 1024; 1 us.
 //
 // Rows past the end of a sequence in its last tile belong to others.  Where they are rows of a result
 // they are not stored; where they are summed over (queries in the keys' kernel, keys in the other) they

@@ -29,7 +29,7 @@
 // The ring of loads runs on from item to item, and an item's first products start under the end of the one
 // before: a block per item cost 7.5 us (d = 64) to 9 us (128) of coming up and running dry, as much as 5 turns.
 //
-// No unit is full (tensor pipe 55%, SFU 42%, issue slots 53% of the cycles at d = 128): a tile's softmax is a chain of
+// No unit is full (tensor pipe 56%, SFU 42%, issue slots 52% of the cycles at d = 128): a tile's softmax is a chain of
 // waits, and its products and powers, which take about the same time at d = 128 and the powers longer at 64, take turns
 // two tiles deep.  One prompt of 16384 tokens, 32 heads of 128: 2.1 ms, 1.05 PFLOP/s of visible pairs (three
 // quarters of what a library product sustains under the power limit); 8 packed prompts of 64 to 4096, heads of
